@@ -11,7 +11,8 @@ joint projection among them.
 
 Work goes to torch's current stream, or to ``stream``, under which outputs and
 scratch are then allocated too; a tensor that another stream made or will free
-has to be ordered by the caller, as with any torch operator.
+has to be ordered by the caller, as with any torch operator.  Every tensor of a
+call, an operator's own included, is on the current device.
 """
 from __future__ import annotations
 
@@ -34,20 +35,26 @@ def _on_stream(call):
     return run
 
 
-def _heads(name: str, t: torch.Tensor, shape: tuple, dtype: torch.dtype) -> bytes:
-    """The view of a checked [tokens, heads, head_dim] tensor."""
+def _heads(name: str, t: torch.Tensor, shape: tuple, dtype: torch.dtype, gpu: int) -> bytes:
+    """The view of a checked [tokens, heads, head_dim] tensor; gpu: the current device, on which the call will run."""
     s = t.stride()
-    if t.shape != shape or t.dtype is not dtype or not t.is_cuda or (s[2] != 1 and shape[2] > 1 and t.numel()):
-        raise ValueError(f"{name}: expected {list(shape)} of {dtype} on the GPU with a dense last dimension, got "
-                         f"{list(t.shape)} of {t.dtype} on {t.device}, strides {s}")
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != gpu or (s[2] != 1 and shape[2] > 1 and t.numel()):
+        raise ValueError(f"{name}: expected {list(shape)} of {dtype} on GPU {gpu} (the current one) with a dense last "
+                         f"dimension, got {list(t.shape)} of {t.dtype} on {t.device}, strides {s}")
     return dq.heads_bytes(t.data_ptr(), s[0], s[1])
 
 
-def _vector(name: str, t: torch.Tensor, n: int, dtypes: tuple) -> torch.Tensor:
-    if t.dim() != 1 or t.shape[0] != n or t.dtype not in dtypes or not t.is_cuda or (n > 1 and t.stride(0) != 1):
-        raise ValueError(f"{name}: expected {n} dense values of {' or '.join(map(str, dtypes))} on the GPU, got "
-                         f"{list(t.shape)} of {t.dtype} on {t.device}")
+def _vector(name: str, t: torch.Tensor, n: int, dtypes: tuple, gpu: int) -> torch.Tensor:
+    if t.dim() != 1 or t.shape[0] != n or t.dtype not in dtypes or t.get_device() != gpu or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name}: expected {n} dense values of {' or '.join(map(str, dtypes))} on GPU {gpu} (the current "
+                         f"one), got {list(t.shape)} of {t.dtype} on {t.device}")
     return t
+
+
+def _own(name: str, t: torch.Tensor, gpu: int):
+    """An operator's own tensor has to be where the call will run."""
+    if t.get_device() != gpu:
+        raise ValueError(f"the operator's {name} is on {t.device}, the current device is GPU {gpu}")
 
 
 def rope_table(n_positions: int, rot_dim: int, theta: float = 10000.0, device="cuda") -> torch.Tensor:
@@ -81,52 +88,56 @@ class PackedAttention:
         dq.lib()
         self.status = torch.zeros(1, dtype=torch.int32, device=device)
 
-    def _shape(self, q, cu_seqlens) -> bytes:
+    def _shape(self, q, cu_seqlens, gpu) -> bytes:
         if q.dtype is not torch.bfloat16 and q.dtype is not torch.float16:
             raise ValueError(f"attention takes bf16 or fp16, got {q.dtype}")
         if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
             raise ValueError("cu_seqlens holds one value more than there are sequences")
         n = cu_seqlens.shape[0]
-        _vector("cu_seqlens", cu_seqlens, n, (torch.int32,))
+        _vector("cu_seqlens", cu_seqlens, n, (torch.int32,), gpu)
+        _own("status word", self.status, gpu)
         return dq.attention_bytes(dq.DTYPES[q.dtype], self.n_heads, self.n_kv_heads, self.head_dim, self.causal,
                                   self.scale, q.shape[0], n - 1, cu_seqlens.data_ptr())
 
-    def _lse(self, lse, T):
+    def _lse(self, lse, T, gpu):
         if lse.shape != (self.n_heads, T) or lse.dtype is not torch.float32 or not lse.is_contiguous() \
-                or not lse.is_cuda:
-            raise ValueError(f"lse: expected dense fp32 [{self.n_heads}, {T}] on the GPU")
+                or lse.get_device() != gpu:
+            raise ValueError(f"lse: expected dense fp32 [{self.n_heads}, {T}] on GPU {gpu} (the current one)")
 
     @_on_stream
     def forward(self, q, k, v, cu_seqlens, out=None, lse=None):
         """(out, lse): the attention output, [tokens, n_heads, head_dim], and the log-sum-exp of each row's
         scores, fp32 [n_heads, tokens]."""
-        T, dtype = q.shape[0], q.dtype
+        T, dtype, gpu = q.shape[0], q.dtype, torch.cuda.current_device()
         of_q, of_k = (T, self.n_heads, self.head_dim), (T, self.n_kv_heads, self.head_dim)
-        views = _heads("q", q, of_q, dtype), _heads("k", k, of_k, dtype), _heads("v", v, of_k, dtype)
-        a = self._shape(q, cu_seqlens)
+        views = _heads("q", q, of_q, dtype, gpu), _heads("k", k, of_k, dtype, gpu), _heads("v", v, of_k, dtype, gpu)
+        a = self._shape(q, cu_seqlens, gpu)
         if out is None:
             out = torch.empty(of_q, dtype=dtype, device=q.device)
         if lse is None:
             lse = torch.empty((self.n_heads, T), dtype=torch.float32, device=q.device)
         else:
-            self._lse(lse, T)
+            self._lse(lse, T, gpu)
+        to = _heads("out", out, of_q, dtype, gpu)
         if T:
-            dq.dq_attention_forward(a, *views, _heads("out", out, of_q, dtype), lse, self.status)
+            dq.dq_attention_forward(a, *views, to, lse, self.status)
         return out, lse
 
     @_on_stream
     def backward(self, dout, q, k, v, out, lse, cu_seqlens, dq_=None, dk=None, dv=None):
         """(dq, dk, dv) from the gradient of ``out``, the inputs and the results of ``forward``."""
-        T, dtype, device = q.shape[0], q.dtype, q.device
+        T, dtype, device, gpu = q.shape[0], q.dtype, q.device, torch.cuda.current_device()
         of_q, of_k = (T, self.n_heads, self.head_dim), (T, self.n_kv_heads, self.head_dim)
-        views = [_heads("dout", dout, of_q, dtype), _heads("q", q, of_q, dtype), _heads("k", k, of_k, dtype),
-                 _heads("v", v, of_k, dtype), _heads("out", out, of_q, dtype)]
-        self._lse(lse, T)
-        a = self._shape(q, cu_seqlens)
+        views = [_heads("dout", dout, of_q, dtype, gpu), _heads("q", q, of_q, dtype, gpu),
+                 _heads("k", k, of_k, dtype, gpu), _heads("v", v, of_k, dtype, gpu),
+                 _heads("out", out, of_q, dtype, gpu)]
+        self._lse(lse, T, gpu)
+        a = self._shape(q, cu_seqlens, gpu)
         dq_ = torch.empty(of_q, dtype=dtype, device=device) if dq_ is None else dq_
         dk = torch.empty(of_k, dtype=dtype, device=device) if dk is None else dk
         dv = torch.empty(of_k, dtype=dtype, device=device) if dv is None else dv
-        grads = _heads("dq", dq_, of_q, dtype), _heads("dk", dk, of_k, dtype), _heads("dv", dv, of_k, dtype)
+        grads = (_heads("dq", dq_, of_q, dtype, gpu), _heads("dk", dk, of_k, dtype, gpu),
+                 _heads("dv", dv, of_k, dtype, gpu))
         if T:
             n = dq.dq_attention_backward_workspace_bytes(a)
             ws = torch.empty(n, dtype=torch.uint8, device=device)
@@ -135,6 +146,7 @@ class PackedAttention:
 
     def check_status(self):
         """Raises if a call since the last check reported a device error (synchronises the stream)."""
+        _own("status word", self.status, torch.cuda.current_device())
         s = dq.dq_get_device_status(self.status)
         if s != dq.DQ_DEVICE_OK:
             self.status.zero_()
@@ -164,28 +176,29 @@ class QKNormRope:
         dq.lib()
 
     def _shape(self, q, k, wq, wk, positions):
-        """(parameters, view of q, view of k)."""
-        dtype, D = q.dtype, self.head_dim
+        """(parameters, view of q, view of k, current device)."""
+        dtype, D, gpu = q.dtype, self.head_dim, torch.cuda.current_device()
         if dtype not in dq.DTYPES:
             raise ValueError(f"expected bf16, fp16 or fp32, got {dtype}")
         if q.dim() != 3 or k.dim() != 3:
             raise ValueError("q and k are [tokens, heads, head_dim]")
         (T, H, _), K = q.shape, k.shape[1]
-        of_q, of_k = _heads("q", q, (T, H, D), dtype), _heads("k", k, (T, K, D), dtype)
-        _vector("wq", wq, D, (torch.float32, dtype))
-        _vector("wk", wk, D, (wq.dtype,))
-        _vector("positions", positions, T, (torch.int32,))
+        of_q, of_k = _heads("q", q, (T, H, D), dtype, gpu), _heads("k", k, (T, K, D), dtype, gpu)
+        _vector("wq", wq, D, (torch.float32, dtype), gpu)
+        _vector("wk", wk, D, (wq.dtype,), gpu)
+        _vector("positions", positions, T, (torch.int32,), gpu)
+        _own("table", self.table, gpu)
         rows, rot = self.table.shape
         return dq.norm_rope_bytes(dq.DTYPES[dtype], dq.DTYPES[wq.dtype], H, K, D, rot, self.interleaved, self.eps,
-                                  self.weight_offset, T, rows), of_q, of_k
+                                  self.weight_offset, T, rows), of_q, of_k, gpu
 
     @_on_stream
     def forward(self, q, k, wq, wk, positions, q_out=None, k_out=None):
         """(q_out, k_out); ``positions``: int32, one for each token.  Outputs may be the inputs themselves."""
-        p, of_q, of_k = self._shape(q, k, wq, wk, positions)
+        p, of_q, of_k, gpu = self._shape(q, k, wq, wk, positions)
         q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
         k_out = torch.empty(k.shape, dtype=q.dtype, device=q.device) if k_out is None else k_out
-        to_q, to_k = _heads("q_out", q_out, q.shape, q.dtype), _heads("k_out", k_out, k.shape, q.dtype)
+        to_q, to_k = _heads("q_out", q_out, q.shape, q.dtype, gpu), _heads("k_out", k_out, k.shape, q.dtype, gpu)
         if q.shape[0]:
             dq.dq_qk_norm_rope(p, of_q, of_k, wq, wk, positions, self.table, to_q, to_k)
         return q_out, k_out
@@ -193,17 +206,17 @@ class QKNormRope:
     @_on_stream
     def backward(self, dq_out, dk_out, q, k, wq, wk, positions, dq_=None, dk=None):
         """(dq, dk, dwq, dwk) from the gradients of ``forward``'s results and its inputs."""
-        p, of_q, of_k = self._shape(q, k, wq, wk, positions)
+        p, of_q, of_k, gpu = self._shape(q, k, wq, wk, positions)
         dtype, device = q.dtype, q.device
         dq_ = torch.empty(q.shape, dtype=dtype, device=device) if dq_ is None else dq_
         dk = torch.empty(k.shape, dtype=dtype, device=device) if dk is None else dk
+        views = (_heads("dq_out", dq_out, q.shape, dtype, gpu), _heads("dk_out", dk_out, k.shape, dtype, gpu))
+        grads = _heads("dq", dq_, q.shape, dtype, gpu), _heads("dk", dk, k.shape, dtype, gpu)
         dwq = torch.empty(self.head_dim, dtype=torch.float32, device=device)
         dwk = torch.empty(self.head_dim, dtype=torch.float32, device=device)
         n = dq.dq_qk_norm_rope_backward_workspace_bytes(p)
         ws = torch.empty(n, dtype=torch.uint8, device=device)
-        dq.dq_qk_norm_rope_backward(p, _heads("dq_out", dq_out, q.shape, dtype), _heads("dk_out", dk_out, k.shape, dtype),
-                                    of_q, of_k, wq, wk, positions, self.table, _heads("dq", dq_, q.shape, dtype),
-                                    _heads("dk", dk, k.shape, dtype), dwq, dwk, ws, n)
+        dq.dq_qk_norm_rope_backward(p, *views, of_q, of_k, wq, wk, positions, self.table, *grads, dwq, dwk, ws, n)
         return dq_, dk, dwq, dwk
 
 
@@ -221,13 +234,14 @@ class Dropout:
         dq.lib()
 
     def _run(self, x, residual, out, round):
-        shape, dtype = x.shape, x.dtype
+        shape, dtype, gpu = x.shape, x.dtype, torch.cuda.current_device()
         if dtype not in dq.DTYPES:
             raise ValueError(f"expected bf16, fp16 or fp32, got {dtype}")
         out = torch.empty(shape, dtype=dtype, device=x.device) if out is None else out
         for name, t in (("x", x), ("residual", residual), ("out", out)):
-            if t is not None and (t.shape != shape or t.dtype is not dtype or not t.is_contiguous() or not t.is_cuda):
-                raise ValueError(f"{name}: expected dense {dtype} {list(shape)} on the GPU")
+            if t is not None and (t.shape != shape or t.dtype is not dtype or not t.is_contiguous()
+                                  or t.get_device() != gpu):
+                raise ValueError(f"{name}: expected dense {dtype} {list(shape)} on GPU {gpu} (the current one)")
         dq.dq_dropout_add(dq.dropout_bytes(dq.DTYPES[dtype], self.p, self.site, self.seed, round), x, residual, out,
                           x.numel())
         return out
