@@ -644,7 +644,10 @@ size_t dq_attention_backward_workspace_bytes(const dq_attention *a);
 /* Gradients of dq_attention_forward from dout, its inputs and its results:
  * with P = exp(S - lse), dP = dout v^T and delta = the row sums of dout out,
  * dv = P^T dout, dS = scale P (dP - delta), dq = dS k, dk = dS^T q; dk and
- * dv are summed over the query heads of their key head.
+ * dv are summed over the query heads of their key head.  P and dS are held in
+ * 16 bits for the products; with fp16 they carry powers of two taken from the
+ * norms of dout and v, so that gradients that fp16 can hold neither overflow
+ * nor vanish on the way.
  *   dq: as q; dk, dv: as k.  ws: device scratch, 16-byte aligned. */
 dq_status dq_attention_backward(const dq_attention *a, const dq_heads *dout, const dq_heads *q, const dq_heads *k,
                                 const dq_heads *v, const dq_heads *out, const float *lse, const dq_heads *dq,

@@ -119,7 +119,9 @@ extern "C" size_t dq_attention_backward_workspace_bytes(const dq_attention *a)
 {
     using namespace dq;
     if (check(a) != DQ_OK) return 0;
-    return ((size_t)a->n_heads * (size_t)a->n_tokens * sizeof(float) + 31) / 16 * 16;
+    // delta of each row; fp16: its norms too
+    const size_t arrays = a->dtype == DQ_FP16 ? 3 * (size_t)a->n_heads + (size_t)a->n_kv_heads : (size_t)a->n_heads;
+    return (arrays * (size_t)a->n_tokens * sizeof(float) + 31) / 16 * 16;
 }
 
 extern "C" dq_status dq_attention_backward(const dq_attention *a, const dq_heads *dout, const dq_heads *q,
@@ -141,6 +143,10 @@ extern "C" dq_status dq_attention_backward(const dq_attention *a, const dq_heads
     if (((uintptr_t)lse | (uintptr_t)status_dev) & 3u || (uintptr_t)ws & 15u) return DQ_ERR_ALIGNMENT;
     P.lse = const_cast<float *>(lse);
     P.delta = static_cast<float *>(ws);
+    if (a->dtype == DQ_FP16) {
+        P.row_norms = P.delta + (int64_t)P.n_heads * P.n_tokens;
+        P.tile_norms = P.row_norms + (int64_t)P.n_heads * P.n_tokens;
+    }
     P.status = status_dev;
     if (!make_map(&P.map_q, P.q, P.n_heads, a) || !make_map(&P.map_dout, P.dout, P.n_heads, a) ||
         !make_map(&P.map_k, P.k, P.n_kv, a) || !make_map(&P.map_v, P.v, P.n_kv, a))

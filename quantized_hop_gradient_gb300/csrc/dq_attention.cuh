@@ -15,6 +15,8 @@ struct AttentionParams {
     CUtensorMap map_q, map_k, map_v, map_dout;
     dq_heads q, k, v, out, dout, dqv, dk, dv;
     float *lse, *delta;
+    float *row_norms;          // fp16, backward: |dout| of each row, n_heads x n_tokens
+    float *tile_norms;         // and the largest of each tile, at its first row: of dout, then of v, (n_heads + n_kv) x n_tokens
     int32_t *status;
     const int32_t *cu;
     int32_t n_tokens, n_seqs, n_heads, n_kv, dim, causal;

@@ -16,6 +16,10 @@
 // 64 over 8: 71 and 72 us, tensor pipe 32% and 41%, issue slots 42% and 50%,
 // exp's unit 23% and 23%: the arithmetic between the products, which are half as
 // long there, one tile's at a time.
+#include <float.h>
+
+#include <algorithm>
+
 #include "dq_attention.cuh"
 
 namespace dq {
@@ -25,11 +29,87 @@ using namespace tc;
 
 constexpr float kLog2e = 1.44269504088896340736f;
 
-// bf16: P is held times 2^16 until the last step, so that exp2, which gives 0
-// below 2^-126, loses nothing that bf16 can hold (down to 2^-133).  fp16 ends
-// at 2^-24, far above, and has no room for a factor.
-template <typename T> __host__ __device__ constexpr float p_shift() { return __is_same(T, __nv_bfloat16) ? 16.0f : 0.0f; }
-template <typename T> __host__ __device__ constexpr float p_unshift() { return __is_same(T, __nv_bfloat16) ? 1.0f / 65536.0f : 1.0f; }
+// P is held times a power of two until the last step.  bf16, 2^16: so that
+// exp2, which gives 0 below 2^-126, loses nothing that bf16 can hold (down to
+// 2^-133).  fp16, 2^12: its steps are 2^-24 below 2^-14, which is the average
+// weight of 16,384 keys, and P is at most 1 but for the rounding of scores and
+// lse, to which a factor of 15 is left (scores beyond 10^7).
+template <typename T> __host__ __device__ constexpr float p_shift() { return __is_same(T, __nv_bfloat16) ? 16.0f : 12.0f; }
+template <typename T> __host__ __device__ constexpr float p_unshift() { return __is_same(T, __nv_bfloat16) ? 1.0f / 65536.0f : 1.0f / 4096.0f; }
+
+// ------------------------------------------------------------------ fp16's range
+// dP - delta can pass 65,504 where the gradients do not (12,000 x 128 elements),
+// and dS of small gradients lies below 2^-24 where they do not.  So fp16 holds
+// dS times a power of two F with |dP - delta| F <= 1, times P's 2^12:
+// |dP_ij| <= |dout_i| |v_j|, and delta, a mean of dP, is below the largest, so
+// |dP - delta| <= B = 2 |dout_i| max |v_j|.  dq is summed over keys and takes an
+// F for each row, from the keys that its tile reads; dk is summed over rows and
+// takes one for a tile of keys, from the rows that it reads.  Both depend on
+// their own sequence only.  Norms that are not finite are left out: every
+// gradient that their row or key enters is not finite either.
+__device__ __forceinline__ float range_factor(float bound)   // F in (1 / (2 B), 1 / B]
+{
+    return bound > 0.0f ? __uint_as_float((253u - (__float_as_uint(bound) >> 23)) << 23) : 1.0f;
+}
+__device__ __forceinline__ float range_inverse(float factor) { return __uint_as_float((254u << 23) - __float_as_uint(factor)); }
+
+// The largest of n tiles' norms, `first` being the first one's first row; called by whole warps.
+__device__ __forceinline__ float largest_norm(const float *norms, int64_t first, int n)
+{
+    float m = 0.0f;
+    for (int i = threadIdx.x & 31; i < n; i += 32) m = fmaxf(m, norms[first + (int64_t)i * kTile]);
+    return __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(m)));   // not negative: ordered as their bits are
+}
+
+// Norms of dout's rows and the largest of each tile of dout and v.  Bound by
+// memory, as dout and v are read once more: 12,291 tokens of 32 heads of 128 over
+// 8, 126 MB, 28 us, 4.5 TB/s (the backward pass: 1,405 us without); by the search
+// and the loads behind it when there are few: 300 tokens of 4 heads 7 us.  A warp
+// takes 32 rows of a tile, a row on 8 or 16 lanes.
+template <typename T, int BOXES> __global__ void __launch_bounds__(128) attention_norms_kernel(const __grid_constant__ AttentionParams P)
+{
+    constexpr int kLanes = 8 * BOXES, kAtOnce = 32 / kLanes, kLoads = 8;
+    __shared__ float part[4];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane / kLanes, piece = lane % kLanes * 8;
+    Slot S;
+    if (!find_slot(P.cu, P.n_seqs, P.n_tokens, blockIdx.x, kTile, S) || S.padding) return;
+    const int first = S.row + 32 * warp, live = S.len - first;   // rows of this warp that exist
+    for (int y = blockIdx.y; y < P.n_heads + P.n_kv; y += gridDim.y) {
+        const bool is_v = y >= P.n_heads;
+        const Heads<T> x = heads<T>(is_v ? P.v : P.dout);
+        const int h = is_v ? y - P.n_heads : y;
+        float top = 0.0f;
+#pragma unroll 1
+        for (int r0 = 0; r0 < 32; r0 += kLoads * kAtOnce) {
+            Raw8<T> g[kLoads];
+#pragma unroll
+            for (int k = 0; k < kLoads; ++k) {
+                const int r = r0 + k * kAtOnce + sub;
+                g[k] = Raw8<T>{};
+                if (r < live && piece < P.dim) g[k] = load8(x.at(S.lo + first + r, h) + piece);
+            }
+#pragma unroll
+            for (int k = 0; k < kLoads; ++k) {
+                const int r = r0 + k * kAtOnce + sub;
+                const F8 a = widen<T>(g[k]);
+                float sum = 0.0f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) sum = fmaf(a.v[e], a.v[e], sum);
+#pragma unroll
+                for (int m = kLanes / 2; m; m >>= 1) sum += __shfl_xor_sync(kFull, sum, m);
+                const float norm = sum <= FLT_MAX ? sqrtf(sum) : 0.0f;
+                top = fmaxf(top, norm);
+                if (!is_v && piece == 0 && r < live) P.row_norms[(int64_t)h * P.n_tokens + S.lo + first + r] = norm;
+            }
+        }
+        top = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(top)));
+        __syncthreads();   // the last head's are read
+        if (lane == 0) part[warp] = top;
+        __syncthreads();
+        if (threadIdx.x == 0)
+            P.tile_norms[(int64_t)y * P.n_tokens + S.lo + S.row] = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
+    }
+}
 
 // N columns of a thread's own row from tensor memory, and N values packed to
 // 16 bits and stored over the first half of N columns.
@@ -83,7 +163,7 @@ template <int BOXES> struct BarsQ {
     unsigned long long s_full[2], dp_full, ds_ready, delta_ready, done, dq_free;
     uint32_t tmem;
     int abort;
-    float rows[2][kTile];         // lse log2(e) (shifted) and delta of the item's queries
+    float rows[3][kTile];         // lse log2(e) (shifted), delta and (fp16) F of the item's queries
     float delta[kPartsQ][kTile];   // the parts' shares of a delta that comes from P dP
 };
 
@@ -320,7 +400,11 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(k
             const Heads<T> out = heads<T>(P.out), dout = heads<T>(P.dout);
             const int64_t at = (int64_t)it.y * P.n_tokens + it.lo + it.row;
             const int live = it.len - it.row - first;   // rows of this warp that exist
-            float l = 0.0f, d = 0.0f;
+            float l = 0.0f, d = 0.0f, f = 1.0f;
+            if constexpr (!kBf16) {
+                const float v_max = largest_norm(P.tile_norms, (int64_t)(P.n_heads + it.y / group) * P.n_tokens + it.lo, key_tiles(it));
+                if (lane < live) f = range_factor(2.0f * P.row_norms[at + first + lane] * v_max);
+            }
             if (lane < live) l = P.lse[at + first + lane] * kLog2e - p_shift<T>();
             // Where all of a row's keys lie in one tile delta is the sum of P dP instead of dout out, which it equals:
             // the rows with few keys, whose gradients are the largest, are then free of out's rounding to 16 bits
@@ -359,6 +443,7 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(k
             if (items && !(ok = mbar_wait(rows_empty, (items - 1) & 1, abort))) break;
             bars->rows[0][first + lane] = l;
             bars->rows[1][first + lane] = d;
+            if constexpr (!kBf16) bars->rows[2][first + lane] = f;
             __syncwarp();
             if (lane == 0) mbar_arrive(rows_full);
         }
@@ -378,6 +463,7 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(k
             if (!(ok = mbar_wait(rows_full, items & 1, abort))) break;
             const float lse2 = bars->rows[0][r];
             float delta = bars->rows[1][r];
+            const float range = kBf16 ? 1.0f : bars->rows[2][r];
             __syncwarp();
             if (lane == 0) mbar_arrive(rows_empty);
             for (int j = 0; j < n; ++j, ++g) {
@@ -419,10 +505,17 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(k
                     delta = bars->delta[0][r] + bars->delta[1][r];
                     if (part == 0 && row < it.len) P.delta[(int64_t)it.y * P.n_tokens + it.lo + row] = delta;
                 }
-                const float2 d2 = make_float2(-delta, -delta);
+                if constexpr (kBf16) {
+                    const float2 d2 = make_float2(-delta, -delta);
 #pragma unroll
-                for (int i = 0; i < kCols / 2; ++i)
-                    p[i] = f2_mul(p[i], add2(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), d2));
+                    for (int i = 0; i < kCols / 2; ++i)
+                        p[i] = f2_mul(p[i], add2(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), d2));
+                } else {
+                    const float2 f2 = make_float2(range, range), d2 = make_float2(-delta * range, -delta * range);
+#pragma unroll
+                    for (int i = 0; i < kCols / 2; ++i)
+                        p[i] = f2_mul(p[i], f2_fma(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), f2, d2));
+                }
                 store_part<T, kCols>(t_s, p);
                 wait_st();
                 fence_before();
@@ -434,6 +527,7 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(k
             // each part stores its share of the columns
             constexpr int kShare = kDim / kPartsQ;
             const Heads<T> out = heads<T>(P.dqv);
+            const float unrange = kBf16 ? 1.0f : range_inverse(range);
 #pragma unroll
             for (int i = 0; i < kShare; i += 32) {
                 uint32_t o[32];
@@ -444,10 +538,13 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(k
                     __syncwarp();
                     if (lane == 0) mbar_arrive(dq_free);
                 }
-                if (SPLIT)   // in the tiles' place: this block's only item is done
+                if (SPLIT) {   // in the tiles' place: this block's only item is done
+                    if constexpr (!kBf16)
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * unrange);
                     leave_columns(reinterpret_cast<float *>(smem) + r * pitch<kDim>() + kShare * part + i, o, n == 0);
-                else
-                    store_columns(o, P.scale * p_unshift<T>(), out.at(it.lo, it.y), out.ts, it.row + 32 * (warp & 3), it.len,
+                } else
+                    store_columns(o, P.scale * p_unshift<T>() * unrange, out.at(it.lo, it.y), out.ts, it.row + 32 * (warp & 3), it.len,
                                   kShare * part + i, P.dim);
             }
         }
@@ -530,7 +627,8 @@ template <int kRing> struct BarsKV {
     unsigned long long s_full[2], p_ready, dp_full, ds_ready, done;
     uint32_t tmem;
     int abort;
-    float4 rows[2][2][kTile / 4];   // -lse log2(e) (shifted) and -delta of the tile's queries
+    float4 rows[2][2][kTile / 4];   // -lse log2(e) (shifted) and -delta (fp16: times F) of the tile's queries
+    float range[4];                 // fp16: F of item i at i mod 4
 };
 
 template <int BOXES> constexpr int smem_bytes_kv()
@@ -695,8 +793,17 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(t
         // ------------------------------------------------------------ the queries' lse and delta
         if constexpr (BOXES == 1) give_registers<kOtherRegsKV>();
         bool ok = true;
-        for (int step = 0; ok && tiles.next(it);) {
+        for (int step = 0, items = 0; ok && tiles.next(it); ++items) {
             const Queries Q(P, it, rank, split);
+            float range = 1.0f;
+            if constexpr (!kBf16) {
+                // (four places: this warp is at most two steps ahead of the factor's readers)
+                float g = 0.0f;
+                for (int h = it.y * group; h < (it.y + 1) * group; ++h)
+                    g = fmaxf(g, largest_norm(P.tile_norms, (int64_t)h * P.n_tokens + it.lo + Q.tile0 * kTile, Q.per_head));
+                range = range_factor(2.0f * g * largest_norm(P.tile_norms, (int64_t)(P.n_heads + it.y) * P.n_tokens + it.lo, Q.tiles));
+                if (lane == 0) bars->range[items & 3] = range;
+            }
             int head = it.y * group + Q.first / Q.per_head, tile = Q.first % Q.per_head;
             for (int i = 0; i < Q.n; ++i, ++step) {
                 const int first = (Q.tile0 + tile) * kTile;
@@ -708,7 +815,7 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(t
                     const int r = lane + 32 * k;
                     const bool in = first + r < it.len;   // no weight behind the end
                     l[k] = in ? P.lse[at + r] * -kLog2e + p_shift<T>() : -INFINITY;
-                    d[k] = in ? -P.delta[at + r] : 0.0f;
+                    d[k] = in ? -P.delta[at + r] * range : 0.0f;
                 }
                 // the buffer's last readers were done before dk of step - 2, which freed that step's q
                 const int e = 2 * step - 4;
@@ -788,12 +895,16 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(t
                 if (!(ok = mbar_wait(dp_full, i & 1, abort))) break;
                 fence_after();
                 load_part<kCols>(t_g, s);
+                const float range = kBf16 ? 1.0f : bars->range[items & 3];
+                auto minus_delta = [&](int k, float a, float b) {   // (dP - delta) F
+                    const float2 x = make_float2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1]));
+                    return kBf16 ? add2(x, make_float2(a, b)) : f2_fma(x, make_float2(range, range), make_float2(a, b));
+                };
 #pragma unroll
                 for (int k = 0; k < kCols / 2; k += 2) {
                     const float4 d = delta[k / 2];
-                    p[k] = f2_mul(p[k], add2(make_float2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), make_float2(d.x, d.y)));
-                    p[k + 1] = f2_mul(p[k + 1], add2(make_float2(__uint_as_float(s[2 * k + 2]), __uint_as_float(s[2 * k + 3])),
-                                                     make_float2(d.z, d.w)));
+                    p[k] = f2_mul(p[k], minus_delta(k, d.x, d.y));
+                    p[k + 1] = f2_mul(p[k + 1], minus_delta(k + 1, d.z, d.w));
                 }
                 store_part<T, kCols>(t_g, p);
                 wait_st();
@@ -808,7 +919,8 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(t
             const bool is_k = part >= kParts / 2;
             const Heads<T> out = heads<T>(is_k ? P.dk : P.dv);
             T *dst = out.at(it.lo, it.y);
-            const float f = is_k ? P.scale * p_unshift<T>() : p_unshift<T>();
+            const float unrange = kBf16 || SPLIT ? 1.0f : range_inverse(bars->range[items & 3]);   // (a cluster: at the end)
+            const float f = is_k ? P.scale * p_unshift<T>() * unrange : p_unshift<T>();
             const int k0 = part % (kParts / 2) * kShare;
             float *sums = reinterpret_cast<float *>(smem);   // the tiles' place: all products are done
 #pragma unroll 1
@@ -861,7 +973,8 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(t
         static_assert(2 * kSum <= (2 + kRing) * kTileBytes, "accumulators fit the tiles' place");
         if (it.len >= 0 && !*abort) {
             add_up_rows<T, kDim>(smem_addr(smem), rank, split, p_unshift<T>(), dv.at(it.lo, it.y), dv.ts, it.row, it.len, P.dim);
-            add_up_rows<T, kDim>(smem_addr(smem) + kSum, rank, split, P.scale * p_unshift<T>(), dk.at(it.lo, it.y), dk.ts, it.row,
+            const float unrange = kBf16 ? 1.0f : range_inverse(bars->range[0]);   // the same in every block
+            add_up_rows<T, kDim>(smem_addr(smem) + kSum, rank, split, P.scale * p_unshift<T>() * unrange, dk.at(it.lo, it.y), dk.ts, it.row,
                                  it.len, P.dim);
         }
         cluster_sync();
@@ -886,6 +999,13 @@ template <typename T, int STEPS, bool SPLIT> cudaError_t launch_dkv(const Attent
 
 template <typename T, int STEPS> cudaError_t launch(const AttentionParams &P, int64_t slots, cudaStream_t st)
 {
+    if constexpr (__is_same(T, __half)) {
+        attention_norms_kernel<T, boxes(STEPS)>
+            <<<dim3((unsigned)slots, (unsigned)std::min(P.n_heads + P.n_kv, 65535)), 128, 0, st>>>(P);
+        note_launches(1);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
     const int64_t mean_tiles = P.n_seqs ? (P.n_tokens / P.n_seqs + kTile - 1) / kTile : 1;
     AttentionParams Q = P;
     Q.y = P.n_heads;
