@@ -628,6 +628,8 @@ typedef struct {
 } dq_attention;
 
 /* S = scale q k^T under the mask, lse = log sum exp S, out = exp(S - lse) v.
+ * A row whose every score is -inf has no weights: out is 0, lse -inf, and the
+ * row has no part in any gradient.
  *   q, out: n_tokens x n_heads x head_dim; k, v: n_tokens x n_kv_heads x
  *   head_dim; lse: device, n_heads x n_tokens fp32 (natural logarithm).
  *   status_dev: device int32, zero before the first call; a kernel whose

@@ -111,6 +111,13 @@ template <typename T, int BOXES> __global__ void __launch_bounds__(128) attentio
     }
 }
 
+// lse log2(e), less the shift: exp2(S scale log2(e) - this) is P, shifted.  A row
+// without any weight (lse = -inf) has P = 0, as if its lse were infinite.
+template <typename T> __device__ __forceinline__ float scaled_lse(float lse)
+{
+    return lse == -INFINITY ? INFINITY : lse * kLog2e - p_shift<T>();
+}
+
 // N columns of a thread's own row from tensor memory, and N values packed to
 // 16 bits and stored over the first half of N columns.
 template <int N> __device__ __forceinline__ void load_part(uint32_t t, uint32_t *s)
@@ -405,7 +412,7 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(k
                 const float v_max = largest_norm(P.tile_norms, (int64_t)(P.n_heads + it.y / group) * P.n_tokens + it.lo, key_tiles(it));
                 if (lane < live) f = range_factor(2.0f * P.row_norms[at + first + lane] * v_max);
             }
-            if (lane < live) l = P.lse[at + first + lane] * kLog2e - p_shift<T>();
+            if (lane < live) l = scaled_lse<T>(P.lse[at + first + lane]);
             // Where all of a row's keys lie in one tile delta is the sum of P dP instead of dout out, which it equals:
             // the rows with few keys, whose gradients are the largest, are then free of out's rounding to 16 bits
             // (without, dq is off by 1.57 times the rounding of its own storage).
@@ -814,7 +821,7 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(t
                 for (int k = 0; k < kTile / 32; ++k) {
                     const int r = lane + 32 * k;
                     const bool in = first + r < it.len;   // no weight behind the end
-                    l[k] = in ? P.lse[at + r] * -kLog2e + p_shift<T>() : -INFINITY;
+                    l[k] = in ? -scaled_lse<T>(P.lse[at + r]) : -INFINITY;
                     d[k] = in ? -P.delta[at + r] * range : 0.0f;
                 }
                 // the buffer's last readers were done before dk of step - 2, which freed that step's q

@@ -76,6 +76,10 @@ __device__ __forceinline__ float max128(const uint32_t *s)
     return max3(max3(a[0], a[1], a[2]), max3(a[3], a[4], a[5]), fmaxf(a[6], a[7]));
 }
 
+// A row whose every score is -inf has no weights and an output of 0, with an
+// lse of -inf.
+__device__ __forceinline__ float inverse_sum(float total) { return total == 0.0f ? 0.0f : 1.0f / total; }
+
 // The two row tiles of an item; with a cluster, the block's part of their keys.
 struct Rows {
     int head[2], row[2], n[2], hk, first, n_max;   // n: key tiles, from `first` on
@@ -419,7 +423,7 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(k
             if (!(ok = mbar_wait(o_done + 8 * u, (kApart ? done - 1 : items) & 1, abort))) break;
             ++items;
             fence_after();
-            const float total = sum.x + sum.y, inv = 1.0f / total;
+            const float total = sum.x + sum.y, inv = inverse_sum(total);
             const Heads<T> out = heads<T>(P.out);
             T *dst = out.at(it.lo, head);
             const int warp_row = row0 + 32 * (warp & 3);
@@ -500,7 +504,7 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(k
                     o.v[4] = fmaf(f, b.x, o.v[4]); o.v[5] = fmaf(f, b.y, o.v[5]);
                     o.v[6] = fmaf(f, b.z, o.v[6]); o.v[7] = fmaf(f, b.w, o.v[7]);
                 }
-                const float inv = 1.0f / total;
+                const float inv = inverse_sum(total);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) o.v[e] *= inv;
                 store8<T>(out.at(it.lo + row, head) + c, o);
