@@ -640,6 +640,13 @@ typedef struct {
 dq_status dq_attention_forward(const dq_attention *a, const dq_heads *q, const dq_heads *k, const dq_heads *v,
                                const dq_heads *out, float *lse, int32_t *status_dev, void *stream);
 
+/* How long a wait inside the attention kernels may take before the kernel
+ * gives up, in cycles of the SM clock, for the calls that this process makes
+ * from now on: 1 .. 8e9, or 0 for the default of 2e9 (about a second).  A wait
+ * for the next tile of work may take 64 times that.  A test of the path that
+ * gives up sets it low; there is no other reason to. */
+dq_status dq_attention_wait_limit(int64_t cycles);
+
 /* Device bytes dq_attention_backward needs (0 for invalid arguments). */
 size_t dq_attention_backward_workspace_bytes(const dq_attention *a);
 

@@ -28,6 +28,8 @@ dq_status check(const dq_attention *a)
     return (uintptr_t)a->cu_seqlens & 3u ? DQ_ERR_ALIGNMENT : DQ_OK;
 }
 
+std::atomic<int64_t> g_wait_cycles{tc::kWaitCycles};
+
 void fill(AttentionParams &P, const dq_attention *a)
 {
     P.cu = a->cu_seqlens;
@@ -39,6 +41,7 @@ void fill(AttentionParams &P, const dq_attention *a)
     P.causal = a->causal;
     P.scale = a->scale;
     P.scale_log2 = (float)((double)a->scale * 1.4426950408889634074);
+    P.wait_cycles = g_wait_cycles.load(std::memory_order_relaxed);
 }
 
 // The driver's tensor-map encoder, looked up once.
@@ -113,6 +116,14 @@ extern "C" dq_status dq_attention_forward(const dq_attention *a, const dq_heads 
     return launch_attention_forward(P, a->dtype == DQ_BF16, static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? DQ_OK
                : DQ_ERR_CUDA;
+}
+
+extern "C" dq_status dq_attention_wait_limit(int64_t cycles)
+{
+    using namespace dq;
+    if (cycles < 0 || cycles > 4 * tc::kWaitCycles) return DQ_ERR_INVALID_ARG;
+    g_wait_cycles.store(cycles ? cycles : tc::kWaitCycles, std::memory_order_relaxed);
+    return DQ_OK;
 }
 
 extern "C" size_t dq_attention_backward_workspace_bytes(const dq_attention *a)

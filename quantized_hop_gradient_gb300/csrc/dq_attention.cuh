@@ -25,6 +25,7 @@ struct AttentionParams {
     int32_t pair_heads;        // a block's two row tiles: two heads, or two tiles of a head
     int32_t ordered;           // tiles are taken in the order of their work over all sequences
     int32_t split;             // blocks (a cluster) that share a tile's loop: 1, 2, 4 or 8
+    long long wait_cycles;       // bound of a wait
 };
 
 // The kernels are built for heads of up to 64, 96 and 128 elements: products
@@ -148,7 +149,7 @@ __device__ __forceinline__ void init_queue(ItemQueue *q, int readers)
 // sequence.
 struct Taker {
     ItemQueue *q;
-    volatile int *abort;
+    tc::Waits waits;
     unsigned block;
     int published = 0, asked = 0;
     bool own = true;    // the block's own index is still to be done
@@ -167,7 +168,11 @@ struct Taker {
                 more = false;
             } else if (!own) {
                 if (lane == 0) tc::claim_block(answer, claim);
-                if (!tc::mbar_wait(claim, asked++ & 1, abort)) return false;
+                if (!tc::mbar_wait(claim, asked & 1, waits)) {
+                    tc::mbar_land(claim, asked & 1);   // the answer, before this block's memory goes
+                    return false;
+                }
+                ++asked;
                 more = tc::claimed_block(answer, block);
                 tc::fence_smem_to_async();   // read before the next answer is written
                 __syncwarp();
@@ -185,7 +190,7 @@ struct Taker {
         }
         if (!more) it = Item{0, -1, 0, 0};
         const int s = published & 1;
-        if (published >= 2 && !tc::mbar_wait(smem_addr(&q->empty[s]), (published / 2 - 1) & 1, abort)) return false;
+        if (published >= 2 && !tc::mbar_wait(smem_addr(&q->empty[s]), (published / 2 - 1) & 1, waits)) return false;
         if (lane == 0) {
             q->item[s] = it;
             tc::mbar_arrive(smem_addr(&q->full[s]));
@@ -199,14 +204,14 @@ struct Taker {
 // The other warps' (or threads') view of the queue.
 struct Tiles {
     ItemQueue *q;
-    volatile int *abort;
+    tc::Waits waits;
     int read = 0;
     // false when there is no more work or a wait ran out
     template <bool ONE = false> __device__ __forceinline__ bool next(Item &it)
     {
         const int s = read & 1;
         const uint32_t full = smem_addr(&q->full[s]), parity = (read >> 1) & 1;
-        if (!(ONE ? tc::mbar_wait_one(full, parity, abort, tc::kQueueCycles) : tc::mbar_wait(full, parity, abort, tc::kQueueCycles)))
+        if (!(ONE ? tc::mbar_wait_one(full, parity, waits, tc::kQueueTimes) : tc::mbar_wait(full, parity, waits, tc::kQueueTimes)))
             return false;
         it = q->item[s];
         if (!ONE) __syncwarp();

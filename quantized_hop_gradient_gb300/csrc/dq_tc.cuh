@@ -16,7 +16,13 @@ namespace tc {
 constexpr int kTile = 128;                 // rows of a tile, lanes of tensor memory
 constexpr int kBoxBytes = kTile * 128;
 constexpr long long kWaitCycles = 2000000000ll;   // bound of a wait: about a second
-constexpr long long kQueueCycles = 64 * kWaitCycles;   // of one for work, which may be far (a long padding)
+constexpr int kQueueTimes = 64;   // as many times that for a wait for work, which may be far (a long padding)
+
+// What the waits of a block share.
+struct Waits {
+    volatile int *out;   // in shared memory: one ran out, every role gives up
+    long long cycles;    // how long one may take
+};
 
 // ---- mbarriers
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count)
@@ -43,25 +49,34 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity)
     return ok != 0;
 }
 
-// Waits for the phase of that parity.  False once `abort` is set or the time
-// is up, which sets it, so that every role of the block gives up together.
-__device__ __forceinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, volatile int *abort, long long most)
+// Waits for the phase of that parity.  False once a wait of the block ran out
+// or this one does, so that every role of the block gives up together.
+__device__ __forceinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, const Waits &waits, int times)
 {
     const long long start = clock64();
     while (!mbar_try(bar, parity)) {
-        if (*abort) return false;
-        if (clock64() - start > most) {
-            *abort = 1;
+        if (*waits.out) return false;
+        if (clock64() - start > waits.cycles * times) {
+            *waits.out = 1;
             return false;
         }
     }
     return true;
 }
 // Called by whole warps; the answer is the same in every lane.
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int *abort, long long most = kWaitCycles)
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, const Waits &waits, int times = 1)
 {
     if (__all_sync(0xFFFFFFFFu, mbar_try(bar, parity))) return true;
-    return __all_sync(0xFFFFFFFFu, mbar_wait_slow(bar, parity, abort, most));
+    return __all_sync(0xFFFFFFFFu, mbar_wait_slow(bar, parity, waits, times));
+}
+// For a block that gives up: waits, still with a limit, until what it has sent
+// off has landed.  Called by whole warps.  A barrier that was never used counts as landed: its phase
+// before the first is odd.
+__device__ __forceinline__ void mbar_land(uint32_t bar, uint32_t parity)
+{
+    const long long start = clock64();
+    while (!__all_sync(0xFFFFFFFFu, mbar_try(bar, parity) || clock64() - start > kWaitCycles)) {
+    }
 }
 
 // Register split between warpgroups; the shares must add up to what the block
@@ -76,10 +91,9 @@ template <int REGS> __device__ __forceinline__ void give_registers()
 }
 
 // The same by a single thread.
-__device__ __forceinline__ bool mbar_wait_one(uint32_t bar, uint32_t parity, volatile int *abort,
-                                              long long most = kWaitCycles)
+__device__ __forceinline__ bool mbar_wait_one(uint32_t bar, uint32_t parity, const Waits &waits, int times = 1)
 {
-    return mbar_try(bar, parity) || mbar_wait_slow(bar, parity, abort, most);
+    return mbar_try(bar, parity) || mbar_wait_slow(bar, parity, waits, times);
 }
 // One thread of a converged warp, the same each time.
 __device__ __forceinline__ bool elect_one()
