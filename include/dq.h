@@ -640,12 +640,11 @@ typedef struct {
 dq_status dq_attention_forward(const dq_attention *a, const dq_heads *q, const dq_heads *k, const dq_heads *v,
                                const dq_heads *out, float *lse, int32_t *status_dev, void *stream);
 
-/* How long a wait inside the attention kernels may take before the kernel
- * gives up, in cycles of the SM clock, for the calls that this process makes
- * from now on: 1 .. 8e9, or 0 for the default of 2e9 (about a second).  A wait
- * for the next tile of work may take 64 times that.  A test of the path that
- * gives up sets it low; there is no other reason to. */
-dq_status dq_attention_wait_limit(int64_t cycles);
+/* Test of the path on which the attention kernels give up.  on = 1: in the
+ * calls that this process makes from now on no wait inside a kernel waits;
+ * the first one that is not over at once makes its block give up, and every
+ * block reports DQ_DEVICE_WAIT_TIMEOUT.  on = 0: as usual. */
+dq_status dq_attention_give_up_selftest(int32_t on);
 
 /* Device bytes dq_attention_backward needs (0 for invalid arguments). */
 size_t dq_attention_backward_workspace_bytes(const dq_attention *a);

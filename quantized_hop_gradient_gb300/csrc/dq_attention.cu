@@ -28,7 +28,7 @@ dq_status check(const dq_attention *a)
     return (uintptr_t)a->cu_seqlens & 3u ? DQ_ERR_ALIGNMENT : DQ_OK;
 }
 
-std::atomic<int64_t> g_wait_cycles{tc::kWaitCycles};
+std::atomic<int32_t> g_give_up{0};   // dq_attention_give_up_selftest
 
 void fill(AttentionParams &P, const dq_attention *a)
 {
@@ -41,7 +41,7 @@ void fill(AttentionParams &P, const dq_attention *a)
     P.causal = a->causal;
     P.scale = a->scale;
     P.scale_log2 = (float)((double)a->scale * 1.4426950408889634074);
-    P.wait_cycles = g_wait_cycles.load(std::memory_order_relaxed);
+    P.give_up = g_give_up.load(std::memory_order_relaxed);
 }
 
 // The driver's tensor-map encoder, looked up once.
@@ -118,11 +118,10 @@ extern "C" dq_status dq_attention_forward(const dq_attention *a, const dq_heads 
                : DQ_ERR_CUDA;
 }
 
-extern "C" dq_status dq_attention_wait_limit(int64_t cycles)
+extern "C" dq_status dq_attention_give_up_selftest(int32_t on)
 {
-    using namespace dq;
-    if (cycles < 0 || cycles > 4 * tc::kWaitCycles) return DQ_ERR_INVALID_ARG;
-    g_wait_cycles.store(cycles ? cycles : tc::kWaitCycles, std::memory_order_relaxed);
+    if (on != 0 && on != 1) return DQ_ERR_INVALID_ARG;
+    dq::g_give_up.store(on, std::memory_order_relaxed);
     return DQ_OK;
 }
 

@@ -25,7 +25,7 @@ struct AttentionParams {
     int32_t pair_heads;        // a block's two row tiles: two heads, or two tiles of a head
     int32_t ordered;           // tiles are taken in the order of their work over all sequences
     int32_t split;             // blocks (a cluster) that share a tile's loop: 1, 2, 4 or 8
-    long long wait_cycles;       // bound of a wait
+    int32_t give_up;           // 1: waits have run out from the start (a test)
 };
 
 // The kernels are built for heads of up to 64, 96 and 128 elements: products
@@ -149,7 +149,7 @@ __device__ __forceinline__ void init_queue(ItemQueue *q, int readers)
 // sequence.
 struct Taker {
     ItemQueue *q;
-    tc::Waits waits;
+    volatile int *abort;
     unsigned block;
     int published = 0, asked = 0;
     bool own = true;    // the block's own index is still to be done
@@ -168,7 +168,7 @@ struct Taker {
                 more = false;
             } else if (!own) {
                 if (lane == 0) tc::claim_block(answer, claim);
-                if (!tc::mbar_wait(claim, asked & 1, waits)) {
+                if (!tc::mbar_wait(claim, asked & 1, abort)) {
                     tc::mbar_land(claim, asked & 1);   // the answer, before this block's memory goes
                     return false;
                 }
@@ -190,7 +190,7 @@ struct Taker {
         }
         if (!more) it = Item{0, -1, 0, 0};
         const int s = published & 1;
-        if (published >= 2 && !tc::mbar_wait(smem_addr(&q->empty[s]), (published / 2 - 1) & 1, waits)) return false;
+        if (published >= 2 && !tc::mbar_wait(smem_addr(&q->empty[s]), (published / 2 - 1) & 1, abort)) return false;
         if (lane == 0) {
             q->item[s] = it;
             tc::mbar_arrive(smem_addr(&q->full[s]));
@@ -204,14 +204,14 @@ struct Taker {
 // The other warps' (or threads') view of the queue.
 struct Tiles {
     ItemQueue *q;
-    tc::Waits waits;
+    volatile int *abort;
     int read = 0;
     // false when there is no more work or a wait ran out
     template <bool ONE = false> __device__ __forceinline__ bool next(Item &it)
     {
         const int s = read & 1;
         const uint32_t full = smem_addr(&q->full[s]), parity = (read >> 1) & 1;
-        if (!(ONE ? tc::mbar_wait_one(full, parity, waits, tc::kQueueTimes) : tc::mbar_wait(full, parity, waits, tc::kQueueTimes)))
+        if (!(ONE ? tc::mbar_wait_one(full, parity, abort, tc::kQueueCycles) : tc::mbar_wait(full, parity, abort, tc::kQueueCycles)))
             return false;
         it = q->item[s];
         if (!ONE) __syncwarp();

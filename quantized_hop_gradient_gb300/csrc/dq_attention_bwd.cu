@@ -163,7 +163,7 @@ template <int BOXES> struct BarsQ {
     unsigned long long v_full[stages_v<BOXES>()], v_empty[stages_v<BOXES>()], rows_full, rows_empty;
     unsigned long long s_full[2], dp_full, ds_ready, delta_ready, done, dq_free, drained;
     uint32_t tmem;
-    int out_of_time;
+    int abort;
     float rows[3][kTile];         // lse log2(e) (shifted), delta and (fp16) F of the item's queries
     float delta[kPartsQ][kTile];   // the parts' shares of a delta that comes from P dP
 };
@@ -195,7 +195,7 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(k
     const uint32_t rows_full = smem_addr(&bars->rows_full), rows_empty = smem_addr(&bars->rows_empty);
     const uint32_t delta_ready = smem_addr(&bars->delta_ready), done = smem_addr(&bars->done);
     const uint32_t dq_free = smem_addr(&bars->dq_free);
-    const Waits waits{&bars->out_of_time, P.wait_cycles};
+    volatile int *abort = &bars->abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (warp == kCopyWarp) {
@@ -226,7 +226,7 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(k
             mbar_init(done, 1);
             mbar_init(dq_free, 4 * kPartsQ);
             mbar_init(smem_addr(&bars->drained), 1);
-            bars->out_of_time = 0;
+            bars->abort = P.give_up;
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         }
     } else if (warp == kProductWarp) {
@@ -237,7 +237,7 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(k
     fence_after();
     const uint32_t tmem = bars->tmem, t_dp = tmem + 2 * kTile, t_dq = tmem + 3 * kTile;   // S: two buffers from 0
     const int group = P.n_heads / P.n_kv;
-    Tiles tiles{&bars->queue, waits};
+    Tiles tiles{&bars->queue, abort};
     Item it;
     const int split = SPLIT ? P.split : 1, rank = SPLIT ? cluster_rank() : 0;
     auto key_tiles = [&](const Item &x) { return ((P.causal ? min(x.row + kTile, x.len) : x.len) + kTile - 1) / kTile; };
@@ -254,7 +254,7 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(k
         auto padding = [&](const Slot &S, int y) {
             if (rank == 0) zero_heads<T>(P.dqv, S.lo + S.row, min(kTile, S.len - S.row), y, P.dim);
         };
-        Taker taker{&bars->queue, waits, blockIdx.x / split};
+        Taker taker{&bars->queue, abort, blockIdx.x / split};
         taker.claims = !SPLIT;   // a cluster does its one tile
         bool ok = true;
         int n = 0, hk = 0, j0 = 0;
@@ -262,7 +262,7 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(k
             const Part part = part_of(it);
             n = part.n, j0 = SPLIT ? part.first : 0, hk = it.y / group;
             if (SPLIT && !n) return true;
-            if (copied_q && !mbar_wait(q_empty, (copied_q - 1) & 1, waits)) return false;
+            if (copied_q && !mbar_wait(q_empty, (copied_q - 1) & 1, abort)) return false;
             if (lane == 0) {
                 mbar_expect(q_full, 2 * kTileBytes);
                 for (int b = 0; b < BOXES; ++b) {
@@ -274,7 +274,7 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(k
             return true;
         };
         auto copy = [&](int j) {
-            if (rk.laps && !mbar_wait(k_empty + 8 * rk.stage, rk.phase ^ 1, waits)) return false;
+            if (rk.laps && !mbar_wait(k_empty + 8 * rk.stage, rk.phase ^ 1, abort)) return false;
             if (lane == 0) {
                 mbar_expect(k_full + 8 * rk.stage, kTileBytes);
                 for (int b = 0; b < BOXES; ++b)
@@ -283,7 +283,7 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(k
             }
             __syncwarp();
             rk.step();
-            if (rv.laps && !mbar_wait(v_empty + 8 * rv.stage, rv.phase ^ 1, waits)) return false;
+            if (rv.laps && !mbar_wait(v_empty + 8 * rv.stage, rv.phase ^ 1, abort)) return false;
             if (lane == 0) {
                 mbar_expect(v_full + 8 * rv.stage, kTileBytes);
                 for (int b = 0; b < BOXES; ++b)
@@ -332,7 +332,7 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(k
                 const int n = part_of(it).n;
                 if (SPLIT && !n) continue;
                 auto scores = [&]() {      // S of the next tile, into the buffers in turn
-                    if (!mbar_wait_one(k_clear + 8 * rk.stage, rk.phase, waits)) return false;
+                    if (!mbar_wait_one(k_clear + 8 * rk.stage, rk.phase, abort)) return false;
                     product_abt<STEPS>(tmem + (scored & 1) * kTile, o_q, o_k + rk.stage * kTileBytes, kInstrS);
                     commit(s_full + 8 * (scored & 1));
                     ++scored;
@@ -347,7 +347,7 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(k
                     ++begun;
                     rv.step();
                 };
-                if (!(ok = mbar_wait_one(q_full, items & 1, waits) && scores() && mbar_wait_one(v_full + 8 * rv.stage, rv.phase, waits)))
+                if (!(ok = mbar_wait_one(q_full, items & 1, abort) && scores() && mbar_wait_one(v_full + 8 * rv.stage, rv.phase, abort)))
                     break;
                 if (n > 1) {
                     grads(0);
@@ -356,12 +356,12 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(k
                     grads(0);
                 }
                 for (int j = 0; j < n; ++j) {
-                    if (j + 1 < n && !(ok = mbar_wait_one(v_full + 8 * rv.stage, rv.phase, waits))) break;
-                    if (!(ok = mbar_wait_one(ds_ready, used & 1, waits))) break;
+                    if (j + 1 < n && !(ok = mbar_wait_one(v_full + 8 * rv.stage, rv.phase, abort))) break;
+                    if (!(ok = mbar_wait_one(ds_ready, used & 1, abort))) break;
                     fence_after();
                     // dP of the next tile first: the threads need it next, and they are done with this one's
                     if (j + 1 < n) grads(j + 1);
-                    if (j == 0 && items && !(ok = mbar_wait_one(dq_free, (items - 1) & 1, waits))) break;   // read
+                    if (j == 0 && items && !(ok = mbar_wait_one(dq_free, (items - 1) & 1, abort))) break;   // read
                     if (j == 0) fence_after();
                     product_ab<kPartsQ>(t_dq, tmem + (used & 1) * kTile, o_k + rd.stage * kTileBytes, kInstrD, j > 0);
                     commit(k_empty + 8 * rd.stage);
@@ -383,7 +383,7 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(k
         while (ok && tiles.next(it)) {
             const Part part = part_of(it);
             for (int j = part.first; j < part.first + part.n; ++j) {
-                if (!(ok = mbar_wait(k_full + 8 * rk.stage, rk.phase, waits))) break;
+                if (!(ok = mbar_wait(k_full + 8 * rk.stage, rk.phase, abort))) break;
                 if ((j + 1) * kTile > it.len) zero_rows<BOXES>(s_k + rk.stage * kTileBytes, it.len - j * kTile, lane);
                 if (lane == 0) mbar_arrive(k_clear + 8 * rk.stage);
                 __syncwarp();
@@ -442,7 +442,7 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(k
                 }
                 if (lane < live && rank == 0) P.delta[at + first + lane] = d;
             }
-            if (items && !(ok = mbar_wait(rows_empty, (items - 1) & 1, waits))) break;
+            if (items && !(ok = mbar_wait(rows_empty, (items - 1) & 1, abort))) break;
             bars->rows[0][first + lane] = l;
             bars->rows[1][first + lane] = d;
             if constexpr (!kBf16) bars->rows[2][first + lane] = f;
@@ -462,14 +462,14 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(k
             const Part part_j = part_of(it);
             const int n = part_j.n, j0 = SPLIT ? part_j.first : 0, row = it.row + r;
             const bool lone = key_tiles(it) == 1;   // delta from the one tile
-            if (!(ok = mbar_wait(rows_full, items & 1, waits))) break;
+            if (!(ok = mbar_wait(rows_full, items & 1, abort))) break;
             const float lse2 = bars->rows[0][r];
             float delta = bars->rows[1][r];
             const float range = kBf16 ? 1.0f : bars->rows[2][r];
             __syncwarp();
             if (lane == 0) mbar_arrive(rows_empty);
             for (int j = 0; j < n; ++j, ++g) {
-                if (!(ok = mbar_wait(s_full + 8 * (g & 1), (g >> 1) & 1, waits))) break;
+                if (!(ok = mbar_wait(s_full + 8 * (g & 1), (g >> 1) & 1, abort))) break;
                 fence_after();
                 const uint32_t t_s = tmem + (g & 1) * kTile + kCols * part + lanes;
                 uint32_t s[kCols];
@@ -482,7 +482,7 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(k
                     p[i].x = exp2_fast(p[i].x);
                     p[i].y = exp2_fast(p[i].y);
                 }
-                if (!(ok = mbar_wait(dp_full, g & 1, waits))) break;
+                if (!(ok = mbar_wait(dp_full, g & 1, abort))) break;
                 fence_after();
                 load_part<kCols>(t_dp + kCols * part + lanes, s);
                 const int first = (j0 + j) * kTile + kCols * part;   // keys that the row does not see
@@ -503,7 +503,7 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(k
                     bars->delta[part][r] = (sum.x + sum.y) * p_unshift<T>();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(delta_ready);
-                    if (!(ok = mbar_wait(delta_ready, shared++ & 1, waits))) break;
+                    if (!(ok = mbar_wait(delta_ready, shared++ & 1, abort))) break;
                     delta = bars->delta[0][r] + bars->delta[1][r];
                     if (part == 0 && row < it.len) P.delta[(int64_t)it.y * P.n_tokens + it.lo + row] = delta;
                 }
@@ -524,7 +524,7 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(k
                 __syncwarp();
                 if (lane == 0) mbar_arrive(ds_ready);
             }
-            if (!ok || !(ok = (SPLIT && !n) || mbar_wait(done, items & 1, waits))) break;
+            if (!ok || !(ok = (SPLIT && !n) || mbar_wait(done, items & 1, abort))) break;
             fence_after();
             // each part stores its share of the columns
             constexpr int kShare = kDim / kPartsQ;
@@ -554,7 +554,7 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(k
 
     fence_before();
     __syncthreads();
-    if (*waits.out) {   // let this block's own copies and products land before its memory goes
+    if (*abort) {   // let this block's own copies and products land before its memory goes
         if (warp == kCopyWarp) {
             mbar_land(q_full, (copied_q - 1) & 1);
             for (int i = 0; i < kK; ++i, rk.step()) mbar_land(k_full + 8 * rk.stage, rk.phase ^ 1);
@@ -578,7 +578,7 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(k
             give_registers<kLaunchRegsQ>();
         cluster_sync();
         it = bars->queue.item[0];   // the one item, if the cluster had any
-        if (it.len >= 0 && !*waits.out) {
+        if (it.len >= 0 && !*abort) {
             const Heads<T> out = heads<T>(P.dqv);
             add_up_rows<T, kDim>(smem_addr(smem), rank, split, P.scale * p_unshift<T>(), out.at(it.lo, it.y), out.ts, it.row, it.len,
                                  P.dim);
@@ -626,7 +626,7 @@ template <int kRing> struct BarsKV {
     unsigned long long kv_full, kv_empty, sums_free, full[kRing], clear[kRing], empty[kRing], rows_full[2];
     unsigned long long s_full[2], p_ready, dp_full, ds_ready, done, drained;
     uint32_t tmem;
-    int out_of_time;
+    int abort;
     float4 rows[2][2][kTile / 4];   // -lse log2(e) (shifted) and -delta (fp16: times F) of the tile's queries
     float range[4];                 // fp16: F of item i at i mod 4
 };
@@ -655,7 +655,7 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(t
     const uint32_t rows_full = smem_addr(bars->rows_full), s_full = smem_addr(bars->s_full);
     const uint32_t p_ready = smem_addr(&bars->p_ready), dp_full = smem_addr(&bars->dp_full);
     const uint32_t ds_ready = smem_addr(&bars->ds_ready), done = smem_addr(&bars->done);
-    const Waits waits{&bars->out_of_time, P.wait_cycles};
+    volatile int *abort = &bars->abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     const uint32_t kv_empty = smem_addr(&bars->kv_empty), sums_free = smem_addr(&bars->sums_free);
@@ -685,7 +685,7 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(t
             mbar_init(ds_ready, 4 * kParts);
             mbar_init(done, 1);
             mbar_init(smem_addr(&bars->drained), 1);
-            bars->out_of_time = 0;
+            bars->abort = P.give_up;
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         }
     } else if (warp == kProductWarp) {
@@ -696,7 +696,7 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(t
     fence_after();
     const uint32_t tmem = bars->tmem, t_dp = tmem + kLead * kTile, t_dv = t_dp + kTile, t_dk = t_dv + kDim;
     auto t_s = [&](int i) { return tmem + i % kLead * kTile; };
-    Tiles tiles{&bars->queue, waits};
+    Tiles tiles{&bars->queue, abort};
     Item it;
     int loaded = 0, items = 0;   // copies issued into the ring, items begun (copy warp)
     // steps are counted over all items: step s is in buffers s % kLead and s & 1, and its tiles are the ring's 2 s and 2 s + 1
@@ -710,13 +710,13 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(t
             zero_heads<T>(P.dk, S.lo + S.row, min(kTile, S.len - S.row), y, P.dim);
             zero_heads<T>(P.dv, S.lo + S.row, min(kTile, S.len - S.row), y, P.dim);
         };
-        Taker taker{&bars->queue, waits, blockIdx.x / split};
+        Taker taker{&bars->queue, abort, blockIdx.x / split};
         taker.claims = !SPLIT;   // a cluster does its one tile
         bool ok = true;
         while (ok && taker.next<true, false>(P, slots, kTile, it, padding)) {
             const Queries Q(P, it, rank, split);
             if (SPLIT && !Q.n) continue;
-            if (items && !(ok = mbar_wait(kv_empty, (items - 1) & 1, waits))) break;
+            if (items && !(ok = mbar_wait(kv_empty, (items - 1) & 1, abort))) break;
             if (lane == 0) {
                 mbar_expect(kv_full, 2 * kTileBytes);
                 for (int b = 0; b < BOXES; ++b) {
@@ -728,7 +728,7 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(t
             int head = it.y * group + Q.first / Q.per_head, at = Q.first % Q.per_head;   // of the step
             for (int e = 0; e < 2 * Q.n; ++e, ++loaded) {
                 const int st = loaded % kRing;
-                if (loaded >= kRing && !(ok = mbar_wait(empty + 8 * st, (loaded / kRing - 1) & 1, waits))) break;
+                if (loaded >= kRing && !(ok = mbar_wait(empty + 8 * st, (loaded / kRing - 1) & 1, abort))) break;
                 if (lane == 0) {
                     mbar_expect(full + 8 * st, kTileBytes);
                     for (int b = 0; b < BOXES; ++b)
@@ -746,7 +746,7 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(t
         if (elect_one()) {   // (alone: with a second condition the compiler no longer sees one thread, 843 us for 798)
             const uint32_t o_k = operand<SPLIT>(s_k), o_v = operand<SPLIT>(s_v), o_ring = operand<SPLIT>(s_ring);
             auto landed = [&](int e) {
-                return mbar_wait_one(clear + 8 * (e % kRing), (e / kRing) & 1, waits);
+                return mbar_wait_one(clear + 8 * (e % kRing), (e / kRing) & 1, abort);
             };
             auto tile = [&](int e) { return o_ring + e % kRing * kTileBytes; };
             auto scores = [&](int i) {   // S^T = k q^T
@@ -766,16 +766,16 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(t
                 const int n = Queries(P, it, rank, split).n;
                 if (SPLIT && !n) continue;
                 // (S and dP of the first step go over the last item's P and dS: products run in the order of their issue)
-                ok = mbar_wait_one(kv_full, items & 1, waits) && scores(s0) && grads(s0) && (kLead == 1 || n < 2 || scores(s0 + 1));
+                ok = mbar_wait_one(kv_full, items & 1, abort) && scores(s0) && grads(s0) && (kLead == 1 || n < 2 || scores(s0 + 1));
                 if (ok && n == 1) commit(kv_empty);
                 for (int i = s0; i < s0 + n && ok; ++i) {
-                    if (!(ok = mbar_wait_one(p_ready, i & 1, waits))) break;
-                    if (i == s0 && items && !(ok = mbar_wait_one(sums_free, (items - 1) & 1, waits))) break;   // read
+                    if (!(ok = mbar_wait_one(p_ready, i & 1, abort))) break;
+                    if (i == s0 && items && !(ok = mbar_wait_one(sums_free, (items - 1) & 1, abort))) break;   // read
                     fence_after();
                     product_ab<kParts>(t_dv, t_s(i), tile(2 * i + 1), kInstrD, i > s0);
                     commit(empty + 8 * ((2 * i + 1) % kRing));
                     if (i + kLead < s0 + n && !(ok = scores(i + kLead))) break;   // over P
-                    if (!(ok = mbar_wait_one(ds_ready, i & 1, waits))) break;
+                    if (!(ok = mbar_wait_one(ds_ready, i & 1, abort))) break;
                     fence_after();
                     product_ab<kParts>(t_dk, t_dp, tile(2 * i), kInstrD, i > s0);
                     commit(empty + 8 * (2 * i % kRing));
@@ -820,7 +820,7 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(t
                 }
                 // the buffer's last readers were done before dk of step - 2, which freed that step's q
                 const int e = 2 * step - 4;
-                if (step >= 2 && !(ok = mbar_wait(empty + 8 * (e % kRing), (e / kRing) & 1, waits))) break;
+                if (step >= 2 && !(ok = mbar_wait(empty + 8 * (e % kRing), (e / kRing) & 1, abort))) break;
                 float *rows = reinterpret_cast<float *>(bars->rows[step & 1]);
 #pragma unroll
                 for (int k = 0; k < kTile / 32; ++k) {
@@ -841,7 +841,7 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(t
             const Queries Q(P, it, rank, split);
             for (int e = 0; e < 2 * Q.n; ++e, ++cleared) {
                 const int st = cleared % kRing;
-                if (!(ok = mbar_wait(full + 8 * st, (cleared / kRing) & 1, waits))) break;
+                if (!(ok = mbar_wait(full + 8 * st, (cleared / kRing) & 1, abort))) break;
                 if (Q.ragged && (Q.first + (e >> 1)) % Q.per_head == Q.per_head - 1)
                     zero_rows<BOXES>(s_ring + st * kTileBytes, it.len - (Q.tiles - 1) * kTile, lane);
                 if (lane == 0) mbar_arrive(clear + 8 * st);
@@ -860,8 +860,8 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(t
             const int row = it.row + r, n = Q.n;
             int at = Q.first % Q.per_head;
             for (int j = Q.first; j < Q.first + n; ++j, ++i) {
-                if (!(ok = mbar_wait(rows_full + 8 * (i & 1), (i >> 1) & 1, waits) &&
-                          mbar_wait(s_full + 8 * (i % kLead), (i / kLead) & 1, waits)))
+                if (!(ok = mbar_wait(rows_full + 8 * (i & 1), (i >> 1) & 1, abort) &&
+                          mbar_wait(s_full + 8 * (i % kLead), (i / kLead) & 1, abort)))
                     break;
                 fence_after();
                 const float4 *lse = bars->rows[i & 1][0] + kCols / 4 * part, *delta = bars->rows[i & 1][1] + kCols / 4 * part;
@@ -893,7 +893,7 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(t
                 fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(p_ready);
-                if (!(ok = mbar_wait(dp_full, i & 1, waits))) break;
+                if (!(ok = mbar_wait(dp_full, i & 1, abort))) break;
                 fence_after();
                 load_part<kCols>(t_g, s);
                 const float range = kBf16 ? 1.0f : bars->range[items & 3];
@@ -913,7 +913,7 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(t
                 __syncwarp();
                 if (lane == 0) mbar_arrive(ds_ready);
             }
-            if (!ok || !(ok = (SPLIT && !n) || mbar_wait(done, items & 1, waits))) break;
+            if (!ok || !(ok = (SPLIT && !n) || mbar_wait(done, items & 1, abort))) break;
             fence_after();
             // half the parts store dv, half dk, each its share of the columns
             constexpr int kShare = 2 * kDim / kParts;
@@ -944,7 +944,7 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(t
 
     fence_before();
     __syncthreads();
-    if (*waits.out) {
+    if (*abort) {
         if (warp == kCopyWarp) {
             mbar_land(kv_full, (items - 1) & 1);
             for (int e = max(0, loaded - kRing); e < loaded; ++e) mbar_land(full + 8 * (e % kRing), (e / kRing) & 1);
@@ -971,7 +971,7 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(t
         const Heads<T> dv = heads<T>(P.dv), dk = heads<T>(P.dk);
         constexpr uint32_t kSum = kTile * pitch<kDim>() * 4;
         static_assert(2 * kSum <= (2 + kRing) * kTileBytes, "accumulators fit the tiles' place");
-        if (it.len >= 0 && !*waits.out) {
+        if (it.len >= 0 && !*abort) {
             add_up_rows<T, kDim>(smem_addr(smem), rank, split, p_unshift<T>(), dv.at(it.lo, it.y), dv.ts, it.row, it.len, P.dim);
             const float unrange = kBf16 ? 1.0f : range_inverse(bars->range[0]);   // the same in every block
             add_up_rows<T, kDim>(smem_addr(smem) + kSum, rank, split, P.scale * p_unshift<T>() * unrange, dk.at(it.lo, it.y), dk.ts, it.row,

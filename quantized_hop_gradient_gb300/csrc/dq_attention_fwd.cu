@@ -52,7 +52,7 @@ template <int BOXES> struct Bars {
     unsigned long long s_full[2], s_free[2], p_ready[2], o_done[2], o_free[2], all_done;
     unsigned long long drained[2];   // a block that gives up: the products of row tile 0 and 1
     uint32_t tmem;
-    int out_of_time;
+    int abort;
     int lead;   // items of which row tile 0 has its first weights
 };
 
@@ -129,8 +129,7 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(k
     const uint32_t s_free = smem_addr(bars->s_free), p_ready = smem_addr(bars->p_ready);
     const uint32_t o_done = smem_addr(bars->o_done), o_free = smem_addr(bars->o_free);
     const uint32_t all_done = smem_addr(&bars->all_done);   // a cluster's block: the products of both row tiles
-    const uint32_t drained = smem_addr(bars->drained);
-    const Waits waits{&bars->out_of_time, P.wait_cycles};
+    volatile int *abort = &bars->abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (warp == kCopyWarp) {
@@ -158,9 +157,9 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(k
                 mbar_init(v_empty + 8 * i, 2);
             }
             mbar_init(all_done, kProductWarps);
-            mbar_init(drained, 1);
-            mbar_init(drained + 8, 1);
-            bars->out_of_time = bars->lead = 0;
+            for (int u = 0; u < kProductWarps; ++u) mbar_init(smem_addr(&bars->drained[u]), 1);
+            bars->abort = P.give_up;
+            bars->lead = 0;
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         }
     } else if (warp == 0) {
@@ -170,7 +169,7 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(k
     __syncthreads();
     fence_after();
     const uint32_t tmem = bars->tmem;
-    Tiles tiles{&bars->queue, waits};
+    Tiles tiles{&bars->queue, abort};
     Item it;
     const int split = SPLIT ? P.split : 1, rank = SPLIT ? cluster_rank() : 0;
     Ring<kK> rk;          // key tiles: copied (copy warp) or consumed (product warps)
@@ -191,14 +190,14 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(k
                     P.lse[(int64_t)R.head[u] * P.n_tokens + S.lo + R.row[u] + i] = -INFINITY;
             }
         };
-        Taker taker{&bars->queue, waits, blockIdx.x / split};
+        Taker taker{&bars->queue, abort, blockIdx.x / split};
         taker.claims = !SPLIT;   // a cluster does its one tile
         bool ok = true;
         while (ok && taker.next<true, true>(P, slots, rows, it, padding)) {
             const Rows R(P, it, rank, split);
             for (int u = 0; u < 2; ++u) {
                 if (!R.n[u]) continue;
-                if (loaded_q[u] && !(ok = mbar_wait(q_empty + 8 * u, (loaded_q[u] - 1) & 1, waits))) break;
+                if (loaded_q[u] && !(ok = mbar_wait(q_empty + 8 * u, (loaded_q[u] - 1) & 1, abort))) break;
                 if (lane == 0) {
                     mbar_expect(q_full + 8 * u, kTileBytes);
                     for (int b = 0; b < BOXES; ++b)
@@ -208,7 +207,7 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(k
                 ++loaded_q[u];
             }
             for (int j = 0; ok && j < R.n_max; ++j) {
-                if (rk.laps && !(ok = mbar_wait(k_empty + 8 * rk.stage, rk.phase ^ 1, waits))) break;
+                if (rk.laps && !(ok = mbar_wait(k_empty + 8 * rk.stage, rk.phase ^ 1, abort))) break;
                 if (lane == 0) {
                     mbar_expect(k_full + 8 * rk.stage, kTileBytes);
                     for (int b = 0; b < BOXES; ++b)
@@ -217,7 +216,7 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(k
                 }
                 __syncwarp();
                 rk.step();
-                if (rv.laps && !(ok = mbar_wait(v_empty + 8 * rv.stage, rv.phase ^ 1, waits))) break;
+                if (rv.laps && !(ok = mbar_wait(v_empty + 8 * rv.stage, rv.phase ^ 1, abort))) break;
                 if (lane == 0) {
                     mbar_expect(v_full + 8 * rv.stage, kTileBytes);
                     for (int b = 0; b < BOXES; ++b)
@@ -244,9 +243,9 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(k
                 const int n = u ? R.n[1] : R.n[0], n_max = R.n_max;
                 // S of key tile j, which is then given back
                 auto scores = [&](int j) {
-                    if (!mbar_wait_one(k_full + 8 * rk.stage, rk.phase, waits)) return false;
+                    if (!mbar_wait_one(k_full + 8 * rk.stage, rk.phase, abort)) return false;
                     if (j < n) {
-                        if (kApart && scored && !mbar_wait_one(s_free + 8 * u, (scored - 1) & 1, waits)) return false;
+                        if (kApart && scored && !mbar_wait_one(s_free + 8 * u, (scored - 1) & 1, abort)) return false;
                         fence_after();
                         product_abt<STEPS>(t_s, tile_q, o_k + rk.stage * kTileBytes, kInstrS);
                         commit(s_full + 8 * u);
@@ -271,15 +270,15 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(k
                     while (*(volatile int *)&bars->lead <= (int)items && clock64() - start < 4096) {
                     }
                 }
-                if (n && !(ok = mbar_wait_one(q_full + 8 * u, items & 1, waits))) break;
+                if (n && !(ok = mbar_wait_one(q_full + 8 * u, items & 1, abort))) break;
                 if (!(ok = scores(0))) break;
                 for (int j = 0; j < n_max; ++j) {
                     if (kApart && j + 1 < n_max && !(ok = scores(j + 1))) break;
-                    if (!(ok = mbar_wait_one(v_clear + 8 * rv.stage, rv.phase, waits))) break;
+                    if (!(ok = mbar_wait_one(v_clear + 8 * rv.stage, rv.phase, abort))) break;
                     if (j < n) {
                         // the last item's O has been read
-                        if (j == 0 && items && !(ok = mbar_wait_one(o_free + 8 * u, (items - 1) & 1, waits))) break;
-                        if (!(ok = mbar_wait_one(p_ready + 8 * u, summed & 1, waits))) break;
+                        if (j == 0 && items && !(ok = mbar_wait_one(o_free + 8 * u, (items - 1) & 1, abort))) break;
+                        if (!(ok = mbar_wait_one(p_ready + 8 * u, summed & 1, abort))) break;
                         fence_after();
                         product_ab<1>(t_o, t_p, o_v + rv.stage * kTileBytes, kInstrO, j > 0);
                         commit(v_empty + 8 * rv.stage);
@@ -307,7 +306,7 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(k
             const Rows R(P, it, rank, split);
             for (int j = 0; j < R.n_max; ++j) {
                 const int behind = it.len - (R.first + j) * kTile;
-                if (!(ok = mbar_wait(v_full + 8 * rv.stage, rv.phase, waits))) break;
+                if (!(ok = mbar_wait(v_full + 8 * rv.stage, rv.phase, abort))) break;
                 if (behind < kTile) zero_rows<BOXES>(s_v + rv.stage * kTileBytes, behind, lane);
                 if (lane == 0) mbar_arrive(v_clear + 8 * rv.stage);
                 __syncwarp();
@@ -341,7 +340,7 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(k
             float m = -INFINITY;
             float2 sum = make_float2(0.0f, 0.0f);
             for (int j = 0; j < n; ++j, ++done) {
-                if (!(ok = mbar_wait(s_full + 8 * u, done & 1, waits))) break;
+                if (!(ok = mbar_wait(s_full + 8 * u, done & 1, abort))) break;
                 fence_after();
                 uint32_t s[128];
 #pragma unroll
@@ -365,7 +364,7 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(k
                 const bool grown = (top - m) * c > kGrowth;
                 if (__any_sync(kFull, grown)) {
                     // O must be at rest; where P lies over S, this tile's S was issued behind the last O += P v
-                    if (kApart && !(ok = mbar_wait(o_done + 8 * u, (done - 1) & 1, waits))) break;
+                    if (kApart && !(ok = mbar_wait(o_done + 8 * u, (done - 1) & 1, abort))) break;
                     fence_after();
                     const float f = grown ? exp2_fast((m - top) * c) : 1.0f;
                     if (grown) m = top;
@@ -395,7 +394,7 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(k
                     if (!kApart && i % 16 == 15) tmem_store16(t_p + i - 15, p + i - 15);
                 }
                 if (kApart) {   // P waits in registers for the last O += P v to be done with its place
-                    if (j > 0 && !(ok = mbar_wait(o_done + 8 * u, (done - 1) & 1, waits))) break;
+                    if (j > 0 && !(ok = mbar_wait(o_done + 8 * u, (done - 1) & 1, abort))) break;
                     fence_after();
                     tmem_store32(t_p, p);
                     tmem_store32(t_p + 32, p + 32);
@@ -409,7 +408,7 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(k
             if (!ok) break;
             if (SPLIT) {
                 // O as it is, with the row's reference and sum, in the tiles' place once all products are done
-                if (!(ok = mbar_wait(all_done, 0, waits))) break;
+                if (!(ok = mbar_wait(all_done, 0, abort))) break;
                 fence_after();
                 float *sums = reinterpret_cast<float *>(smem) + (u * kTile + (int)(threadIdx.x & 127)) * pitch<kDim>();
 #pragma unroll 1
@@ -424,7 +423,7 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(k
                 ml[2 * kTile] = sum.x + sum.y;
                 continue;
             }
-            if (!(ok = mbar_wait(o_done + 8 * u, (kApart ? done - 1 : items) & 1, waits))) break;
+            if (!(ok = mbar_wait(o_done + 8 * u, (kApart ? done - 1 : items) & 1, abort))) break;
             ++items;
             fence_after();
             const float total = sum.x + sum.y, inv = inverse_sum(total);
@@ -450,7 +449,7 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(k
 
     fence_before();
     __syncthreads();
-    if (*waits.out) {
+    if (*abort) {
         // a wait ran out: let this block's own copies and products land before its memory goes
         if (warp == kCopyWarp) {
             for (int u = 0; u < 2; ++u) mbar_land(q_full + 8 * u, (loaded_q[u] - 1) & 1);
@@ -458,9 +457,10 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(k
             for (int i = 0; i < kV; ++i, rv.step()) mbar_land(v_full + 8 * rv.stage, rv.phase ^ 1);
             if (lane == 0) *P.status = DQ_DEVICE_WAIT_TIMEOUT;
         } else if (warp < kProductWarps) {
-            if (elect_one()) commit(drained + 8 * warp);
+            const uint32_t bar = smem_addr(&bars->drained[warp]);
+            if (elect_one()) commit(bar);
             __syncwarp();
-            mbar_land(drained + 8 * warp, 0);
+            mbar_land(bar, 0);
         }
         __syncthreads();
     }
@@ -477,7 +477,7 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(k
             give_registers<kLaunchRegs>();
         cluster_sync();
         it = bars->queue.item[0];   // the one item, if the cluster had any
-        if (it.len >= 0 && !*waits.out) {
+        if (it.len >= 0 && !*abort) {
             const Rows R(P, it, 0, 1);
             const Heads<T> out = heads<T>(P.out);
             const int share = kTile / split, pieces = kDim / 8;

@@ -16,13 +16,9 @@ namespace tc {
 constexpr int kTile = 128;                 // rows of a tile, lanes of tensor memory
 constexpr int kBoxBytes = kTile * 128;
 constexpr long long kWaitCycles = 2000000000ll;   // bound of a wait: about a second
-constexpr int kQueueTimes = 64;   // as many times that for a wait for work, which may be far (a long padding)
-
-// What the waits of a block share.
-struct Waits {
-    volatile int *out;   // in shared memory: one ran out, every role gives up
-    long long cycles;    // how long one may take
-};
+// Of one for work, which may be far: empty slots and padding are passed over at 8.6 ns a block of the grid (32 million
+// blocks in 276 ms), 18 s for the largest grid.
+constexpr long long kQueueCycles = 64 * kWaitCycles;
 
 // ---- mbarriers
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count)
@@ -49,29 +45,30 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity)
     return ok != 0;
 }
 
-// Waits for the phase of that parity.  False once a wait of the block ran out
-// or this one does, so that every role of the block gives up together.
-__device__ __forceinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, const Waits &waits, int times)
+// Waits for the phase of that parity.  False once `abort` is set or the time
+// is up, which sets it, so that every role of the block gives up together.
+__device__ __forceinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, volatile int *abort, long long most)
 {
     const long long start = clock64();
     while (!mbar_try(bar, parity)) {
-        if (*waits.out) return false;
-        if (clock64() - start > waits.cycles * times) {
-            *waits.out = 1;
+        if (*abort) return false;
+        if (clock64() - start > most) {
+            *abort = 1;
             return false;
         }
     }
     return true;
 }
 // Called by whole warps; the answer is the same in every lane.
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, const Waits &waits, int times = 1)
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int *abort, long long most = kWaitCycles)
 {
     if (__all_sync(0xFFFFFFFFu, mbar_try(bar, parity))) return true;
-    return __all_sync(0xFFFFFFFFu, mbar_wait_slow(bar, parity, waits, times));
+    return __all_sync(0xFFFFFFFFu, mbar_wait_slow(bar, parity, abort, most));
 }
+
 // For a block that gives up: waits, still with a limit, until what it has sent
-// off has landed.  Called by whole warps.  A barrier that was never used counts as landed: its phase
-// before the first is odd.
+// off has landed.  Called by whole warps.  A barrier that was never used counts
+// as landed: its phase before the first is odd.
 __device__ __forceinline__ void mbar_land(uint32_t bar, uint32_t parity)
 {
     const long long start = clock64();
@@ -91,9 +88,10 @@ template <int REGS> __device__ __forceinline__ void give_registers()
 }
 
 // The same by a single thread.
-__device__ __forceinline__ bool mbar_wait_one(uint32_t bar, uint32_t parity, const Waits &waits, int times = 1)
+__device__ __forceinline__ bool mbar_wait_one(uint32_t bar, uint32_t parity, volatile int *abort,
+                                              long long most = kWaitCycles)
 {
-    return mbar_try(bar, parity) || mbar_wait_slow(bar, parity, waits, times);
+    return mbar_try(bar, parity) || mbar_wait_slow(bar, parity, abort, most);
 }
 // One thread of a converged warp, the same each time.
 __device__ __forceinline__ bool elect_one()

@@ -178,7 +178,7 @@ _SIGS = {
     "dq_mx_exchange": ([C.c_int32, C.c_int32, C.c_void_p, C.c_int64, C.c_void_p, C.c_size_t, C.c_void_p,
                         C.c_void_p, C.c_void_p, C.c_void_p], C.c_int),
     "dq_attention_forward": ([C.POINTER(dq_attention), _HEADS, _HEADS, _HEADS, _HEADS, _V, _V, _V], C.c_int),
-    "dq_attention_wait_limit": ([C.c_int64], C.c_int),
+    "dq_attention_give_up_selftest": ([C.c_int32], C.c_int),
     "dq_attention_backward_workspace_bytes": ([C.POINTER(dq_attention)], C.c_size_t),
     "dq_attention_backward": ([C.POINTER(dq_attention), _HEADS, _HEADS, _HEADS, _HEADS, _HEADS, _V, _HEADS, _HEADS,
                                _HEADS, _V, C.c_size_t, _V, _V], C.c_int),
@@ -582,8 +582,8 @@ def dq_attention_forward(a, q, k, v, out, lse, status, stream=None):
     _call("dq_attention_forward", a, q, k, v, out, _ptr(lse), _ptr(status), _stream(stream))
 
 
-def dq_attention_wait_limit(cycles: int):
-    _check(lib().dq_attention_wait_limit(cycles), "dq_attention_wait_limit")
+def dq_attention_give_up_selftest(on: bool):
+    _check(lib().dq_attention_give_up_selftest(on), "dq_attention_give_up_selftest")
 
 
 def dq_attention_backward_workspace_bytes(a) -> int:

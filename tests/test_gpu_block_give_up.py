@@ -1,7 +1,7 @@
 """Attention kernels whose waits run out: the status says so, the call returns, and the next call is right.
 
-The limit of a wait is set to one cycle, so that whatever a block's roles still have to wait for runs out: nothing is
-missing, and every role gives up and returns.  (Waits that are over at once pass, so single blocks may still finish.)"""
+Under the self-test no wait waits, so that every role of a block gives up where it would have waited, with copies, products
+and requests for work in flight.  (Waits that are over at once pass, so single blocks may still finish.)"""
 import pytest
 import torch
 
@@ -19,15 +19,15 @@ def _lib():
 
 @pytest.fixture
 def short():
-    """Calls with the short limit; the default comes back whatever happens."""
+    """Calls under the self-test, which ends with them whatever happens."""
     def run(call):
-        dq.dq_attention_wait_limit(1)
+        dq.dq_attention_give_up_selftest(True)
         try:
             return call()
         finally:
-            dq.dq_attention_wait_limit(0)
+            dq.dq_attention_give_up_selftest(False)
     yield run
-    dq.dq_attention_wait_limit(0)
+    dq.dq_attention_give_up_selftest(False)
 
 
 CASES = [
@@ -66,10 +66,3 @@ def test_waits_that_run_out(lens, H, K, D, dtype, causal, short):
             for a, b in zip(call(), want):
                 assert torch.equal(a, b)
             op.check_status()
-
-
-def test_the_limit_is_checked():
-    for bad in (-1, 8_000_000_001):
-        with pytest.raises(dq.DQError) as e:
-            dq.dq_attention_wait_limit(bad)
-        assert e.value.status == dq.DQ_ERR_INVALID_ARG
