@@ -155,10 +155,12 @@ struct Taker {
     bool own = true;    // the block's own index is still to be done
     bool claims = true; // it may take over others
 
-    // The next tile, published to the readers too; false at the end, or when a wait ran out.
-    // UP: a tile's work grows with its row under the causal mask.
-    template <bool BY_WORK, bool UP, typename Padding>
-    __device__ __forceinline__ bool next(const AttentionParams &P, int slots, int rows, Item &it, Padding padding)
+    enum Found { kTaken, kEnd, kOutOfTime, kNothing };
+
+    // The next tile, published to the readers too, or the end of work, or a wait ran out.  With ONE it looks at one block
+    // only, and publishes nothing if that has no tile.  UP: a tile's work grows with its row under the causal mask.
+    template <bool BY_WORK, bool UP, bool ONE = false, typename Padding>
+    __device__ __forceinline__ Found next(const AttentionParams &P, int slots, int rows, Item &it, Padding padding)
     {
         const int lane = threadIdx.x & 31;
         const uint32_t claim = smem_addr(&q->claim), answer = smem_addr(q->answer);
@@ -170,7 +172,7 @@ struct Taker {
                 if (lane == 0) tc::claim_block(answer, claim);
                 if (!tc::mbar_wait(claim, asked & 1, abort)) {
                     tc::mbar_land(claim, asked & 1);   // the answer, before this block's memory goes
-                    return false;
+                    return kOutOfTime;
                 }
                 ++asked;
                 more = tc::claimed_block(answer, block);
@@ -186,18 +188,19 @@ struct Taker {
                 padding(S, y);
                 found = false;
             }
+            if (ONE && !found) return kNothing;
             it = Item{S.lo, S.len, S.row, y};
         }
         if (!more) it = Item{0, -1, 0, 0};
         const int s = published & 1;
-        if (published >= 2 && !tc::mbar_wait(smem_addr(&q->empty[s]), (published / 2 - 1) & 1, abort)) return false;
+        if (published >= 2 && !tc::mbar_wait(smem_addr(&q->empty[s]), (published / 2 - 1) & 1, abort)) return kOutOfTime;
         if (lane == 0) {
             q->item[s] = it;
             tc::mbar_arrive(smem_addr(&q->full[s]));
         }
         __syncwarp();
         ++published;
-        return more;
+        return more ? kTaken : kEnd;
     }
 };
 

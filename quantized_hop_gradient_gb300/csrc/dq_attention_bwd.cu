@@ -295,20 +295,26 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(k
             return true;
         };
         if constexpr (kAhead == 0) {
-            while (ok && taker.next<false, true>(P, slots, kTile, it, padding)) {
+            while (ok && taker.next<false, true>(P, slots, kTile, it, padding) == Taker::kTaken) {
                 ok = begin();
                 for (int j = 0; ok && j < n; ++j) ok = copy(j);
             }
         } else {
-            // One place that takes an item, at step `ask` of the one before (code that a block runs once or twice is read
-            // from memory; narrow heads in this form: 8 sequences of 1,024 86.7 us, 84 in the plain one).
+            // One place that looks for the next item, from step `ask` of the one before on (code that a block runs once or
+            // twice is read from memory; narrow heads in this form: 8 sequences of 1,024 86.7 us, 84 in the plain one).  One
+            // block's slot for each copy: slots without a tile may be many, and the copies are waited for.
             Item next;
-            bool more = true;
+            Taker::Found found = Taker::kNothing;
             for (int j = 0, ask = 0; ok; ++j) {
-                if (j == ask) more = taker.next<false, true>(P, slots, kTile, next, padding);
+                if (j >= ask && found == Taker::kNothing) {
+                    do found = taker.next<false, true, true>(P, slots, kTile, next, padding);
+                    while (found == Taker::kNothing && j == n);
+                    if (!(ok = found != Taker::kOutOfTime)) break;
+                }
                 if (j == n) {
-                    if (!more) break;
+                    if (found == Taker::kEnd) break;
                     it = next;
+                    found = Taker::kNothing;
                     if (!(ok = begin())) break;
                     j = 0, ask = n > kAhead ? n - kAhead : n;
                     if (SPLIT && !n) {   // the part of a cluster that has no keys
@@ -713,7 +719,7 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(t
         Taker taker{&bars->queue, abort, blockIdx.x / split};
         taker.claims = !SPLIT;   // a cluster does its one tile
         bool ok = true;
-        while (ok && taker.next<true, false>(P, slots, kTile, it, padding)) {
+        while (ok && taker.next<true, false>(P, slots, kTile, it, padding) == Taker::kTaken) {
             const Queries Q(P, it, rank, split);
             if (SPLIT && !Q.n) continue;
             if (items && !(ok = mbar_wait(kv_empty, (items - 1) & 1, abort))) break;

@@ -193,7 +193,7 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(k
         Taker taker{&bars->queue, abort, blockIdx.x / split};
         taker.claims = !SPLIT;   // a cluster does its one tile
         bool ok = true;
-        while (ok && taker.next<true, true>(P, slots, rows, it, padding)) {
+        while (ok && taker.next<true, true>(P, slots, rows, it, padding) == Taker::kTaken) {
             const Rows R(P, it, rank, split);
             for (int u = 0; u < 2; ++u) {
                 if (!R.n[u]) continue;
