@@ -630,7 +630,7 @@ struct Queries {
 template <int kRing> struct BarsKV {
     ItemQueue queue;
     unsigned long long kv_full, kv_empty, sums_free, full[kRing], clear[kRing], empty[kRing], rows_full[2];
-    unsigned long long s_full[2], p_ready, dp_full, ds_ready, done, drained;
+    unsigned long long s_full[2], p_ready[2], dp_full, ds_ready, done, drained;
     uint32_t tmem;
     int abort;
     float4 rows[2][2][kTile / 4];   // -lse log2(e) (shifted) and -delta (fp16: times F) of the tile's queries
@@ -650,7 +650,9 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(t
     constexpr int BOXES = boxes(STEPS);
     constexpr int kDim = 64 * BOXES;
     constexpr int kRing = ring<BOXES>(), kParts = parts_kv<BOXES>(), kCols = kTile / kParts;
-    // Heads of up to 64 elements leave tensor memory for two S: the scores then run two steps ahead.
+    // Heads of up to 64 elements leave tensor memory for two S: the scores then run two steps ahead, and a warp may be done
+    // with P of a step before another one is with P of the step before.  So the steps take turns at two p_ready barriers (dP
+    // of a step follows dS of the one before, by all warps: one ds_ready).
     constexpr int kLead = BOXES == 1 ? 2 : 1;
     constexpr uint32_t kTileBytes = BOXES * kBoxBytes;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -659,7 +661,7 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(t
     const uint32_t kv_full = smem_addr(&bars->kv_full), full = smem_addr(bars->full), clear = smem_addr(bars->clear);
     const uint32_t empty = smem_addr(bars->empty);
     const uint32_t rows_full = smem_addr(bars->rows_full), s_full = smem_addr(bars->s_full);
-    const uint32_t p_ready = smem_addr(&bars->p_ready), dp_full = smem_addr(&bars->dp_full);
+    const uint32_t p_ready = smem_addr(bars->p_ready), dp_full = smem_addr(&bars->dp_full);
     const uint32_t ds_ready = smem_addr(&bars->ds_ready), done = smem_addr(&bars->done);
     volatile int *abort = &bars->abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -687,6 +689,7 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(t
             mbar_init(s_full, 1);
             mbar_init(s_full + 8, 1);
             mbar_init(p_ready, 4 * kParts);
+            mbar_init(p_ready + 8, 4 * kParts);
             mbar_init(dp_full, 1);
             mbar_init(ds_ready, 4 * kParts);
             mbar_init(done, 1);
@@ -775,7 +778,7 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(t
                 ok = mbar_wait_one(kv_full, items & 1, abort) && scores(s0) && grads(s0) && (kLead == 1 || n < 2 || scores(s0 + 1));
                 if (ok && n == 1) commit(kv_empty);
                 for (int i = s0; i < s0 + n && ok; ++i) {
-                    if (!(ok = mbar_wait_one(p_ready, i & 1, abort))) break;
+                    if (!(ok = mbar_wait_one(p_ready + 8 * (i & 1), (i >> 1) & 1, abort))) break;
                     if (i == s0 && items && !(ok = mbar_wait_one(sums_free, (items - 1) & 1, abort))) break;   // read
                     fence_after();
                     product_ab<kParts>(t_dv, t_s(i), tile(2 * i + 1), kInstrD, i > s0);
@@ -898,7 +901,7 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(t
                 wait_st();
                 fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(p_ready);
+                if (lane == 0) mbar_arrive(p_ready + 8 * (i & 1));
                 if (!(ok = mbar_wait(dp_full, i & 1, abort))) break;
                 fence_after();
                 load_part<kCols>(t_g, s);
