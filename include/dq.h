@@ -640,6 +640,15 @@ typedef struct {
 dq_status dq_attention_forward(const dq_attention *a, const dq_heads *q, const dq_heads *k, const dq_heads *v,
                                const dq_heads *out, float *lse, int32_t *status_dev, void *stream);
 
+/* How the kernels of a call are launched on a GPU of n_sms SMs: plan[0] the
+ * forward kernel, [1] dq, [2] dk and dv.  Needs no GPU; for tests and tuning. */
+typedef struct {
+    int64_t blocks;    /* tiles' slots: with more of them than SMs a block works through several */
+    int32_t split;     /* blocks that share a tile's loop: 1, 2, 4 or 8 */
+    int32_t by_work;   /* 1: tiles are taken in the order of their work over all sequences */
+} dq_attention_launch;
+dq_status dq_attention_plan(const dq_attention *a, int32_t n_sms, dq_attention_launch *plan);
+
 /* Test of the path on which the attention kernels give up.  on = 1: in the
  * calls that this process makes from now on no wait inside a kernel waits;
  * the first one that is not over at once makes its block give up, and every

@@ -118,6 +118,19 @@ extern "C" dq_status dq_attention_forward(const dq_attention *a, const dq_heads 
                : DQ_ERR_CUDA;
 }
 
+extern "C" dq_status dq_attention_plan(const dq_attention *a, int32_t n_sms, dq_attention_launch *plan)
+{
+    using namespace dq;
+    const dq_status s = check(a);
+    if (s != DQ_OK) return s;
+    if (n_sms < 1 || n_sms > 65535 || !plan) return DQ_ERR_INVALID_ARG;
+    const Choice c[3] = {choose_forward(a->n_tokens, a->n_seqs, a->n_heads, a->n_kv_heads, n_sms),
+                         choose_dq(a->n_tokens, a->n_seqs, a->n_heads, n_sms),
+                         choose_dkv(a->n_tokens, a->n_seqs, a->n_heads, a->n_kv_heads, n_sms)};
+    for (int i = 0; i < 3; ++i) plan[i] = dq_attention_launch{c[i].blocks, c[i].split, c[i].ordered};
+    return DQ_OK;
+}
+
 extern "C" dq_status dq_attention_give_up_selftest(int32_t on)
 {
     if (on != 0 && on != 1) return DQ_ERR_INVALID_ARG;

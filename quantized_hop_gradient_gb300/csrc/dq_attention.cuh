@@ -372,24 +372,78 @@ __device__ __forceinline__ void add_up_rows(uint32_t acc, int rank, int split, f
 // is better to go sequence by sequence, whose keys and rows then stay in L2: dq
 // of 12,291 tokens in two, 32 heads of 128, 3,168 blocks: 619 us against 597;
 // with one tile or none an SM the order does not matter.
-inline int32_t by_work(int64_t blocks, int64_t n_seqs)
-{
-    return n_seqs <= 31 && blocks > sm_count() && blocks <= 4 * sm_count();
-}
+inline int32_t by_work(int64_t blocks, int64_t n_seqs, int sms) { return n_seqs <= 31 && blocks > sms && blocks <= 4 * sms; }
 
 // How many blocks share a tile: as many as (nearly) all run at once, some slots
 // being empty, up to 8, while each keeps four steps of the loop that a tile of
 // the pack's mean length has (the lengths themselves are not known here):
 // shorter parts cost more than they give, 22 against 12 us for the dk, dv of 38
 // sequences of 54 tokens.
-inline int split_for(int64_t blocks, int64_t steps)
+inline int split_for(int64_t blocks, int64_t steps, int sms)
 {
     int split = 1;
-    while (split < 8 && blocks * split * 2 <= sm_count() * 3 / 2 && split * 8 <= steps) split *= 2;
+    while (split < 8 && blocks * split * 2 <= sms * 3 / 2 && split * 8 <= steps) split *= 2;
     return split;
 }
 
-// Launches `blocks` blocks, or as many clusters of P.split.
+// How a kernel is launched: `blocks` tiles' slots, or as many clusters.
+struct Choice {
+    int64_t blocks;
+    int32_t y, ordered, split;
+};
+
+inline int64_t mean_tiles(int64_t n_tokens, int64_t n_seqs) { return n_seqs ? (n_tokens / n_seqs + tc::kTile - 1) / tc::kTile : 1; }
+
+// The forward kernel takes two heads of a group, or two tiles of one head.
+inline bool pairs_heads(int32_t n_heads, int32_t n_kv) { return n_heads / n_kv % 2 == 0; }
+
+inline Choice choose_forward(int64_t n_tokens, int64_t n_seqs, int32_t n_heads, int32_t n_kv, int sms)
+{
+    const bool pair = pairs_heads(n_heads, n_kv);
+    Choice c{};
+    c.y = pair ? n_heads / 2 : n_heads;
+    c.blocks = slot_count(n_tokens, n_seqs, pair ? tc::kTile : 2 * tc::kTile) * c.y;
+    // Few tiles: the blocks of a cluster share the keys.  bf16, causal, us without and with: one sequence of 2,048, 4/2
+    // heads of 128: 32.5, 23.3; 4,096, 2/1 heads of 64: 40.7, 21.6; 8,192, one head of 128: 95.1, 42.0.  Below 12 key
+    // tiles the cluster's barriers and the joining cost what they give: 1,381, 4/2 heads of 96: 22.0, 22.7.
+    const int64_t steps = mean_tiles(n_tokens, n_seqs);
+    c.ordered = by_work(c.blocks, n_seqs, sms);
+    c.split = steps < 12 ? 1 : split_for(c.blocks, steps, sms);
+    return c;
+}
+
+inline Choice choose_dq(int64_t n_tokens, int64_t n_seqs, int32_t n_heads, int sms)
+{
+    Choice c{};
+    c.y = n_heads;
+    c.blocks = slot_count(n_tokens, n_seqs, tc::kTile) * n_heads;
+    // (by work: many tiles, or few short ones, and nothing gained: 20 sequences of 300, 8 heads: 20.4 us, by work 21.4)
+    c.split = split_for(c.blocks, mean_tiles(n_tokens, n_seqs), sms);
+    return c;
+}
+
+inline Choice choose_dkv(int64_t n_tokens, int64_t n_seqs, int32_t n_heads, int32_t n_kv, int sms)
+{
+    Choice c{};
+    c.y = n_kv;
+    c.blocks = slot_count(n_tokens, n_seqs, tc::kTile) * n_kv;
+    const int64_t steps = mean_tiles(n_tokens, n_seqs);
+    // (the first tile waits for the search: not for short sequences, 43.5 against 41 us for the backward pass of 20 of 300
+    // tokens, 8 heads of 64)
+    c.ordered = steps >= 4 && by_work(c.blocks, n_seqs, sms);
+    c.split = split_for(c.blocks, steps * (n_heads / n_kv), sms);
+    return c;
+}
+
+// The parameters with a choice, and its launch.
+inline AttentionParams chosen(const AttentionParams &P, const Choice &c)
+{
+    AttentionParams Q = P;
+    Q.y = c.y;
+    Q.ordered = c.ordered;
+    Q.split = c.split;
+    return Q;
+}
 inline cudaError_t launch_split(void (*kernel)(AttentionParams), const AttentionParams &P, int64_t blocks, int threads, int smem,
                                 cudaStream_t st)
 {

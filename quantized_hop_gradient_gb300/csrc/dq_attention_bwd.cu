@@ -1015,20 +1015,13 @@ template <typename T, int STEPS> cudaError_t launch(const AttentionParams &P, in
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
-    const int64_t mean_tiles = P.n_seqs ? (P.n_tokens / P.n_seqs + kTile - 1) / kTile : 1;
-    AttentionParams Q = P;
-    Q.y = P.n_heads;
-    // (dq by work: many tiles, or few short ones, and nothing gained: 20 sequences of 300, 8 heads: 20.4 us, by work 21.4)
-    Q.split = split_for(slots * P.n_heads, mean_tiles);
-    const cudaError_t e = Q.split > 1 ? launch_dq<T, STEPS, true>(Q, slots * P.n_heads, st)
-                                      : launch_dq<T, STEPS, false>(Q, slots * P.n_heads, st);
+    const int sms = sm_count();
+    const Choice q = choose_dq(P.n_tokens, P.n_seqs, P.n_heads, sms), kv = choose_dkv(P.n_tokens, P.n_seqs, P.n_heads, P.n_kv, sms);
+    const cudaError_t e = q.split > 1 ? launch_dq<T, STEPS, true>(chosen(P, q), q.blocks, st)
+                                      : launch_dq<T, STEPS, false>(chosen(P, q), q.blocks, st);
     if (e != cudaSuccess) return e;
-    // (the first tile waits for the search: not for short sequences, 43.5 against 41 us for the backward pass of 20 of 300
-    // tokens, 8 heads of 64)
-    Q.ordered = mean_tiles >= 4 && by_work(slots * P.n_kv, P.n_seqs);
-    Q.y = P.n_kv;
-    Q.split = split_for(slots * P.n_kv, mean_tiles * (P.n_heads / P.n_kv));
-    return Q.split > 1 ? launch_dkv<T, STEPS, true>(Q, slots * P.n_kv, st) : launch_dkv<T, STEPS, false>(Q, slots * P.n_kv, st);
+    return kv.split > 1 ? launch_dkv<T, STEPS, true>(chosen(P, kv), kv.blocks, st)
+                        : launch_dkv<T, STEPS, false>(chosen(P, kv), kv.blocks, st);
 }
 
 }  // namespace

@@ -533,17 +533,10 @@ template <typename T> cudaError_t launch_type(const AttentionParams &P, int64_t 
 
 cudaError_t launch_attention_forward(const AttentionParams &P0, bool bf16, cudaStream_t st)
 {
-    AttentionParams P = P0;
-    P.pair_heads = P.n_heads / P.n_kv % 2 == 0;
-    P.y = P.pair_heads ? P.n_heads / 2 : P.n_heads;
-    const int64_t blocks = slot_count(P.n_tokens, P.n_seqs, P.pair_heads ? kTile : 2 * kTile) * P.y;
-    // Few tiles: the blocks of a cluster share the keys.  bf16, causal, us without and with: one sequence of 2,048, 4/2
-    // heads of 128: 32.5, 23.3; 4,096, 2/1 heads of 64: 40.7, 21.6; 8,192, one head of 128: 95.1, 42.0.  Below 12 key
-    // tiles the cluster's barriers and the joining cost what they give: 1,381, 4/2 heads of 96: 22.0, 22.7.
-    const int64_t steps = P.n_seqs ? (P.n_tokens / P.n_seqs + kTile - 1) / kTile : 1;
-    P.ordered = by_work(blocks, P.n_seqs);
-    P.split = steps < 12 ? 1 : split_for(blocks, steps);
-    return bf16 ? launch_type<__nv_bfloat16>(P, blocks, st) : launch_type<__half>(P, blocks, st);
+    const Choice c = choose_forward(P0.n_tokens, P0.n_seqs, P0.n_heads, P0.n_kv, sm_count());
+    AttentionParams P = chosen(P0, c);
+    P.pair_heads = pairs_heads(P.n_heads, P.n_kv);
+    return bf16 ? launch_type<__nv_bfloat16>(P, c.blocks, st) : launch_type<__half>(P, c.blocks, st);
 }
 
 }  // namespace dq

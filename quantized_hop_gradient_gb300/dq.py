@@ -104,6 +104,10 @@ class dq_attention(C.Structure):
                 ("cu_seqlens", C.c_void_p)]
 
 
+class dq_attention_launch(C.Structure):
+    _fields_ = [("blocks", C.c_int64), ("split", C.c_int32), ("by_work", C.c_int32)]
+
+
 class dq_norm_rope(C.Structure):
     _fields_ = [("dtype", C.c_int32), ("weight_dtype", C.c_int32), ("n_heads", C.c_int32), ("n_kv_heads", C.c_int32),
                 ("head_dim", C.c_int32), ("rot_dim", C.c_int32), ("interleaved", C.c_int32), ("eps", C.c_float),
@@ -178,6 +182,7 @@ _SIGS = {
     "dq_mx_exchange": ([C.c_int32, C.c_int32, C.c_void_p, C.c_int64, C.c_void_p, C.c_size_t, C.c_void_p,
                         C.c_void_p, C.c_void_p, C.c_void_p], C.c_int),
     "dq_attention_forward": ([C.POINTER(dq_attention), _HEADS, _HEADS, _HEADS, _HEADS, _V, _V, _V], C.c_int),
+    "dq_attention_plan": ([C.POINTER(dq_attention), C.c_int32, C.c_void_p], C.c_int),
     "dq_attention_give_up_selftest": ([C.c_int32], C.c_int),
     "dq_attention_backward_workspace_bytes": ([C.POINTER(dq_attention)], C.c_size_t),
     "dq_attention_backward": ([C.POINTER(dq_attention), _HEADS, _HEADS, _HEADS, _HEADS, _HEADS, _V, _HEADS, _HEADS,
@@ -580,6 +585,13 @@ def heads(t) -> bytes:
 def dq_attention_forward(a, q, k, v, out, lse, status, stream=None):
     """``a``: attention_bytes(...); q, k, v, out: heads(...)."""
     _call("dq_attention_forward", a, q, k, v, out, _ptr(lse), _ptr(status), _stream(stream))
+
+
+def dq_attention_plan(a, n_sms: int):
+    """The launches of the forward, the dq and the dk, dv kernel: three dq_attention_launch."""
+    plan = (dq_attention_launch * 3)()
+    _call("dq_attention_plan", a if isinstance(a, bytes) else C.byref(a), n_sms, plan)
+    return list(plan)
 
 
 def dq_attention_give_up_selftest(on: bool):
