@@ -16,6 +16,7 @@ call, an operator's own included, is on the current device.
 """
 from __future__ import annotations
 
+import ctypes
 import functools
 import math
 
@@ -33,6 +34,11 @@ def _on_stream(call):
         with torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream):
             return call(self, *args, **kw)
     return run
+
+
+def _fp32(x: float) -> float:
+    """x as the kernels' parameters hold it; what they could not hold is refused where it is given."""
+    return ctypes.c_float(x).value
 
 
 def _heads(name: str, t: torch.Tensor, shape: tuple, dtype: torch.dtype, gpu: int) -> bytes:
@@ -82,9 +88,9 @@ class PackedAttention:
         if head_dim % 8 or not 8 <= head_dim <= 128:
             raise ValueError("head_dim is a multiple of 8 from 8 to 128")
         self.n_heads, self.n_kv_heads, self.head_dim, self.causal = n_heads, n_kv_heads, head_dim, bool(causal)
-        self.scale = 1.0 / math.sqrt(head_dim) if scale is None else float(scale)
-        if not 0.0 < self.scale < math.inf:
-            raise ValueError("scale is positive")
+        self.scale = _fp32(1.0 / math.sqrt(head_dim) if scale is None else scale)
+        if not 0.0 < self.scale <= 3.4e38:
+            raise ValueError("scale is positive and finite in fp32")
         dq.lib()
         self.status = torch.zeros(1, dtype=torch.int32, device=device)
 
@@ -169,10 +175,10 @@ class QKNormRope:
             raise ValueError("table: expected dense fp32 [positions, rot_dim] on the GPU")
         if table.shape[1] % (8 if interleaved else 16) or table.shape[1] > head_dim:
             raise ValueError("rot_dim is at most head_dim and a multiple of 16 (interleaved: of 8)")
-        if not eps > 0:
-            raise ValueError("eps is positive")
-        self.head_dim, self.table, self.eps = head_dim, table, float(eps)
-        self.weight_offset, self.interleaved = float(weight_offset), bool(interleaved)
+        self.head_dim, self.table, self.eps = head_dim, table, _fp32(eps)
+        self.weight_offset, self.interleaved = _fp32(weight_offset), bool(interleaved)
+        if not self.eps > 0 or not math.isfinite(self.weight_offset):
+            raise ValueError("eps is positive and weight_offset finite in fp32")
         dq.lib()
 
     def _shape(self, q, k, wq, wk, positions):
@@ -226,17 +232,20 @@ class Dropout:
     and the element's index, and on nothing else; the backward pass draws it again."""
 
     def __init__(self, p: float, *, seed: int = 0, site: int = 0):
-        if not 0.0 <= p < 1.0 - 2.0 ** -17:
-            raise ValueError("p is at least 0 and below 1 - 2^-17")
+        self.p = _fp32(p)
+        if not 0.0 <= self.p < 1.0 - 2.0 ** -17:
+            raise ValueError("p is at least 0 and below 1 - 2^-17 in fp32")
         if not (0 <= site < 1 << 32 and 0 <= seed < 1 << 64):
             raise ValueError("site has 32 bits, seed 64")
-        self.p, self.seed, self.site = float(p), seed, site
+        self.seed, self.site = seed, site
         dq.lib()
 
     def _run(self, x, residual, out, round):
         shape, dtype, gpu = x.shape, x.dtype, torch.cuda.current_device()
         if dtype not in dq.DTYPES:
             raise ValueError(f"expected bf16, fp16 or fp32, got {dtype}")
+        if not 0 <= round < 1 << 64:
+            raise ValueError("round has 64 bits")
         out = torch.empty(shape, dtype=dtype, device=x.device) if out is None else out
         for name, t in (("x", x), ("residual", residual), ("out", out)):
             if t is not None and (t.shape != shape or t.dtype is not dtype or not t.is_contiguous()
