@@ -506,7 +506,9 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(k
 #pragma unroll
                     for (int i = 0; i < kCols / 2; ++i)
                         sum = f2_fma(p[i], make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), sum);
-                    bars->delta[part][r] = (sum.x + sum.y) * p_unshift<T>();
+                    // (one key: its weight is 1, not exp of a difference of rounded numbers, and dS is 0)
+                    const bool sole = part == 0 && (P.causal ? min(row + 1, it.len) : it.len) == 1;
+                    bars->delta[part][r] = sole ? __uint_as_float(s[0]) : (sum.x + sum.y) * p_unshift<T>();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(delta_ready);
                     if (!(ok = mbar_wait(delta_ready, shared++ & 1, abort))) break;

@@ -150,8 +150,10 @@ class PackedAttention:
             dq.dq_attention_backward(a, *views, lse, *grads, ws, n, self.status)
         return dq_, dk, dv
 
+    @_on_stream
     def check_status(self):
-        """Raises if a call since the last check reported a device error (synchronises the stream)."""
+        """Raises if a call on the current stream, or on ``stream``, reported a device error since the last check, and
+        synchronises that stream.  Calls on other streams count once they are done."""
         _own("status word", self.status, torch.cuda.current_device())
         s = dq.dq_get_device_status(self.status)
         if s != dq.DQ_DEVICE_OK:
@@ -229,7 +231,8 @@ class QKNormRope:
 class Dropout:
     """Dropout at rate ``p`` (realised in steps of 2^-16) with the residual sum.  The mask depends on ``seed``,
     ``site`` (a number of the caller's for the place in the model and the worker), ``round`` (the training step)
-    and the element's index, and on nothing else; the backward pass draws it again."""
+    and the element's index, and on nothing else; the backward pass draws it again.  All of these are numbers on the host:
+    a captured graph draws the mask of the round that it was captured with."""
 
     def __init__(self, p: float, *, seed: int = 0, site: int = 0):
         self.p = _fp32(p)

@@ -66,3 +66,21 @@ def test_waits_that_run_out(lens, H, K, D, dtype, causal, short):
             for a, b in zip(call(), want):
                 assert torch.equal(a, b)
             op.check_status()
+
+
+def test_the_status_of_a_call_on_another_stream(short):
+    """check_status(stream=...) waits for that stream's calls; the current stream's need not have to."""
+    q, k, v, _ = pack([4100], 0, 8, 8, 128, BF16)
+    cu = cu_of([4100])
+    op = layers.PackedAttention(8, 8, 128)
+    op.forward(q, k, v, cu)
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            for _ in range(20):
+                op.forward(q, k, v, cu)                  # some milliseconds before the call that gives up
+        short(lambda: op.forward(q, k, v, cu, stream=stream))
+        with pytest.raises(RuntimeError, match="status 2"):
+            op.check_status(stream=stream)
+        op.check_status(stream=stream)
