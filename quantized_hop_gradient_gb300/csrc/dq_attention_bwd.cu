@@ -53,11 +53,12 @@ __device__ __forceinline__ float range_factor(float bound)   // F in (1 / (2 B),
 }
 __device__ __forceinline__ float range_inverse(float factor) { return __uint_as_float((254u << 23) - __float_as_uint(factor)); }
 
-// The largest of n tiles' norms, `first` being the first one's first row; called by whole warps.
-__device__ __forceinline__ float largest_norm(const float *norms, int64_t first, int n)
+// The largest of the norms of `n` tiles of each of `heads` heads that lie n_tokens apart, `first` being the first one's
+// first row; called by whole warps.
+__device__ __forceinline__ float largest_norm(const float *norms, int64_t first, int n, int heads, int64_t n_tokens)
 {
     float m = 0.0f;
-    for (int i = threadIdx.x & 31; i < n; i += 32) m = fmaxf(m, norms[first + (int64_t)i * kTile]);
+    for (int i = threadIdx.x & 31; i < n * heads; i += 32) m = fmaxf(m, norms[first + i / n * n_tokens + i % n * kTile]);
     return __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(m)));   // not negative: ordered as their bits are
 }
 
@@ -410,7 +411,7 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(k
             const int live = it.len - it.row - first;   // rows of this warp that exist
             float l = 0.0f, d = 0.0f, f = 1.0f;
             if constexpr (!kBf16) {
-                const float v_max = largest_norm(P.tile_norms, (int64_t)(P.n_heads + it.y / group) * P.n_tokens + it.lo, key_tiles(it));
+                const float v_max = largest_norm(P.tile_norms, (int64_t)(P.n_heads + it.y / group) * P.n_tokens + it.lo, key_tiles(it), 1, 0);
                 if (lane < live) f = range_factor(2.0f * P.row_norms[at + first + lane] * v_max);
             }
             if (lane < live) l = scaled_lse<T>(P.lse[at + first + lane]);
@@ -810,10 +811,10 @@ template <typename T, int STEPS, bool SPLIT> __global__ void __launch_bounds__(t
             float range = 1.0f;
             if constexpr (!kBf16) {
                 // (four places: this warp is at most two steps ahead of the factor's readers)
-                float g = 0.0f;
-                for (int h = it.y * group; h < (it.y + 1) * group; ++h)
-                    g = fmaxf(g, largest_norm(P.tile_norms, (int64_t)h * P.n_tokens + it.lo + Q.tile0 * kTile, Q.per_head));
-                range = range_factor(2.0f * g * largest_norm(P.tile_norms, (int64_t)(P.n_heads + it.y) * P.n_tokens + it.lo, Q.tiles));
+                const float v_max = largest_norm(P.tile_norms, (int64_t)(P.n_heads + it.y) * P.n_tokens + it.lo, Q.tiles, 1, 0);
+                range = range_factor(2.0f * v_max *
+                                     largest_norm(P.tile_norms, (int64_t)it.y * group * P.n_tokens + it.lo + Q.tile0 * kTile,
+                                                  Q.per_head, group, P.n_tokens));
                 if (lane == 0) bars->range[items & 3] = range;
             }
             int head = it.y * group + Q.first / Q.per_head, tile = Q.first % Q.per_head;
