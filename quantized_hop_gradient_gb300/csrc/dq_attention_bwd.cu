@@ -4,18 +4,26 @@
 // order of blocks: one owns a tile of queries and sums dq over the keys, one
 // owns a tile of keys and sums dk and dv over the queries and over the heads
 // of its group.  Both compute the scores and dP again: seven products where a
-// single kernel with shared sums would need five.
+// single kernel that adds dq up in turns, key tile by key tile, would need five
+// and as many fp32 additions to memory as there are key tiles.
 //
 //   P = exp(scale q k^T - lse);  dP = dout v^T;  dS = P (dP - delta) scale
 //   delta = sum_j P dP = dout . out;  dq = dS k;  dk = dS^T q;  dv = P^T dout
 //
+// P and dS are rounded to 16 bits because the tensor core multiplies them with
+// 16-bit operands; delta of rows with more than one key tile comes from out as
+// it is stored, in 16 bits, since a sum of P dP would need another pass over
+// the keys.  These roundings are what the gradients' error over the plain
+// 32-bit form's comes from (0.0024 against 0.0017 of their norm in bf16).
+//
 // What bounds them (bf16, causal): 12,291 tokens of 32 heads of 128 over 8: dq
-// 582 us, dk and dv 794 us, 1.75 PFLOP/s over the seven products, 0.92 of the
+// 581 us, dk and dv 783 us, 1.76 PFLOP/s over the seven products, 0.93 of the
 // library's plain product; tensor pipe 78% and 76% active, issue slots 40% and
 // 33%; in a long loop the card is at its power limit.  5,096 tokens of 32 heads of
-// 64 over 8: 71 and 72 us, tensor pipe 32% and 41%, issue slots 42% and 50%,
+// 64 over 8: 71 and 71 us, tensor pipe 32% and 41%, issue slots 42% and 50%,
 // exp's unit 23% and 23%: the arithmetic between the products, which are half as
-// long there, one tile's at a time.
+// long there, one tile's at a time.  fp16, with its factors (below): 28 us of
+// norms, 612 and 814 us; 10, 73 and 75 us.
 #include <float.h>
 
 #include <algorithm>
@@ -44,7 +52,8 @@ template <typename T> __host__ __device__ constexpr float p_unshift() { return _
 // |dP_ij| <= |dout_i| |v_j|, and delta, a mean of dP, is below the largest, so
 // |dP - delta| <= B = 2 |dout_i| max |v_j|.  dq is summed over keys and takes an
 // F for each row, from the keys that its tile reads; dk is summed over rows and
-// takes one for a tile of keys, from the rows that it reads.  Both depend on
+// takes one for a tile of keys, from the rows that it reads (a row whose dout is
+// 2^-20 of the largest one's then loses bits of its share).  Both depend on
 // their own sequence only.  Norms that are not finite are left out: every
 // gradient that their row or key enters is not finite either.
 __device__ __forceinline__ float range_factor(float bound)   // F in (1 / (2 B), 1 / B]
@@ -64,9 +73,9 @@ __device__ __forceinline__ float largest_norm(const float *norms, int64_t first,
 
 // Norms of dout's rows and the largest of each tile of dout and v.  Bound by
 // memory, as dout and v are read once more: 12,291 tokens of 32 heads of 128 over
-// 8, 126 MB, 28 us, 4.5 TB/s (the backward pass: 1,405 us without); by the search
-// and the loads behind it when there are few: 300 tokens of 4 heads 7 us.  A warp
-// takes 32 rows of a tile, a row on 8 or 16 lanes.
+// 8, 126 MB, 28 us, 4.5 TB/s; by the search and the loads behind it when there
+// are few: 300 tokens of 4 heads 7 us.  A warp takes 32 rows of a tile, a row on
+// 8 or 16 lanes.
 template <typename T, int BOXES> __global__ void __launch_bounds__(128) attention_norms_kernel(const __grid_constant__ AttentionParams P)
 {
     constexpr int kLanes = 8 * BOXES, kAtOnce = 32 / kLanes, kLoads = 8;
